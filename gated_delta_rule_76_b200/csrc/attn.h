@@ -1,0 +1,93 @@
+// Launchers of the softmax-attention layer's kernels (entry points in attn_api.cu).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace gdn {
+
+// Norm and rotation of head rows (qk_rope.cu).  A row source or destination of tokens `stride`
+// elements apart; vec: every row starts on a 16-byte boundary.
+struct Rows {
+    const void* p;
+    int64_t stride;
+    int vec;
+};
+
+struct RopeParams {
+    const void *q_w, *k_w;   // [d] norm weights or NULL
+    const float* inv_freq;   // [rot / 2]
+    int rot, interleaved;
+    float eps, rot_scale;
+};
+
+// What kv_append adds to the forward: the rows of k and v go to the cache.
+struct AppendParams {
+    const int32_t *cu, *context, *table;  // cu may be NULL: token t is sequence t's
+    void *k_cache, *v_cache;
+    int64_t num_pages, page_size, max_pages;
+    int nseq;
+};
+
+struct QkParams {
+    Rows q, k, v;              // v: append only
+    const int32_t* positions;  // forward and backward
+    void *q_out, *k_out;       // dense; NULL: not wanted
+    const void *gq, *gk;       // backward: gradients of q_out, k_out (dense)
+    int T, Hq, Hk;
+    RopeParams rope;
+    AppendParams app;
+    float* partials;           // backward: [CTAs][2][d]
+};
+
+cudaError_t qk_norm_rope_fwd(const QkParams& p, int d, bool bf16, cudaStream_t st);
+size_t qk_norm_rope_bwd_partials(int T, int d);  // floats
+// dq_w, dk_w [d] (NULL without the norm)
+cudaError_t qk_norm_rope_bwd(const QkParams& p, int d, bool bf16, void* dq, void* dk, float* dq_w, float* dk_w,
+                             cudaStream_t st);
+cudaError_t kv_append(const QkParams& p, int d, cudaStream_t st);
+
+// Single-token attention over the paged cache (attn_decode.cu).
+struct DecodeAttnParams {
+    const void* q;
+    int64_t q_stride;
+    int q_vec;
+    const void *k_cache, *v_cache;
+    const int32_t *table, *context;
+    void* o;
+    float* part;               // split contexts: [split][N * Hq][d + 2]
+    int64_t num_pages, max_pages, max_context, window;
+    int64_t page_size;
+    int N, Hq, Hk;
+    int chunk, splits;         // tokens a split, splits a sequence
+    float scale;
+};
+void plan_decode_attn(int64_t N, int64_t Hq, int64_t Hk, int64_t reach, int* chunk, int* splits);
+size_t decode_attn_part_floats(int64_t N, int64_t Hq, int64_t d, int splits);
+cudaError_t decode_attn(const DecodeAttnParams& p, int d, cudaStream_t st);
+
+// Causal attention over packed sequences on the tensor cores (attn_fwd.cu, attn_bwd.cu).
+struct AttnIO {
+    Rows q, k, v;              // bf16, 16-byte aligned rows (vec)
+    const int32_t* cu;
+    int T, nseq, Hq, Hk;
+    int64_t window;            // 0: none
+    float scale;
+    void* o;                   // forward: out; backward: the forward's output
+    // the forward's cache: rows' log2-sum-exp2 of the scaled scores, tile-aligned [Hq][tiles][128], and
+    // o - bf16(o) [T,Hq,d] (NULL in a forward that keeps none)
+    float* lse;
+    void* o_lo;
+    // backward
+    const void* grad_o;
+    void *dq, *dk, *dv;
+    float* delta;              // [Hq][tiles][128]: rows' sum of grad_o .* o
+    int* err;                  // device error word
+    uint64_t wait_ns;          // limit of one bounded wait, 0: the default
+};
+// Tiles of 128 rows over all sequences, at most.
+inline int64_t attn_tiles(int64_t T, int64_t nseq) { return T / 128 + (nseq < T ? nseq : T); }
+cudaError_t attn_fwd(const AttnIO& io, int d, cudaStream_t st);
+cudaError_t attn_bwd(const AttnIO& io, int d, cudaStream_t st);
+
+}  // namespace gdn

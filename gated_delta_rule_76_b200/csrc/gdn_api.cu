@@ -6,6 +6,7 @@
 #include <cstring>
 #include <string>
 
+#include "api_util.h"
 #include "gdn.h"
 #include "launch.h"
 
@@ -20,6 +21,7 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 namespace {
 
 thread_local std::string g_last_error;
+}  // namespace
 
 gdn_status fail(gdn_status code, const char* fmt, ...) {
     char buf[512];
@@ -35,40 +37,7 @@ gdn_status cuda_fail(cudaError_t e, const char* where) {
     return fail(GDN_ERR_CUDA, "%s: %s (%s)", where, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-size_t elem_size(int dtype) { return dtype == GDN_F32 ? 4 : 2; }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Buf {
-    const void* p;
-    size_t bytes;
-    const char* name;
-    size_t align = 16;  // required alignment of p (a strided input: its element size)
-};
-
-bool overlaps(const Buf& a, const Buf& b) {
-    if (!a.p || !b.p || !a.bytes || !b.bytes) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// Every output against every input and every other output.
-gdn_status check_buffers(const Buf* in, int nin, const Buf* out, int nout) {
-    for (int i = 0; i < nin; ++i)
-        if (in[i].p && (reinterpret_cast<uintptr_t>(in[i].p) & (in[i].align - 1)))
-            return fail(GDN_ERR_INVALID_ARG, "%s is not %zu-byte aligned", in[i].name, in[i].align);
-    for (int i = 0; i < nout; ++i) {
-        if (out[i].p && !aligned16(out[i].p))
-            return fail(GDN_ERR_INVALID_ARG, "%s is not 16-byte aligned", out[i].name);
-        for (int j = 0; j < nin; ++j)
-            if (overlaps(out[i], in[j]))
-                return fail(GDN_ERR_INVALID_ARG, "output %s overlaps input %s", out[i].name, in[j].name);
-        for (int j = 0; j < i; ++j)
-            if (overlaps(out[i], out[j]))
-                return fail(GDN_ERR_INVALID_ARG, "outputs %s and %s overlap", out[i].name, out[j].name);
-    }
-    return GDN_OK;
-}
+namespace {
 
 // Shared checks of sizes, modes and dtypes.
 gdn_status check_common(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, int64_t dv,
@@ -102,56 +71,6 @@ Problem make_problem(int64_t B, int64_t T, int64_t Hk, int64_t Hv, int64_t dk, i
     pb.scale = scale;
     pb.head_map = head_map;
     return pb;
-}
-
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
-// ---- token strides (gdn_strides) ---------------------------------------------------------
-// A token-major input of `rows` tokens of `row` elements whose tokens are `stride` elements apart
-// (0: dense).  One that is not dense is copied into the workspace before the call's kernels run.
-bool strided(int64_t stride, int64_t row) { return stride != 0 && stride != row; }
-
-// The input as a buffer: from its first to its last element; a strided one needs only the
-// alignment of its element type.
-Buf tok(const void* p, size_t rows, int64_t row, int64_t stride, size_t es, const char* name) {
-    const size_t step = (size_t)(stride ? stride : row);
-    return Buf{p, p && rows ? ((rows - 1) * step + (size_t)row) * es : 0, name, strided(stride, row) ? es : 16};
-}
-
-gdn_status check_stride(int64_t stride, int64_t row, const char* name) {
-    if (stride != 0 && (stride < row || stride > (int64_t(1) << 31)))
-        return fail(GDN_ERR_INVALID_ARG, "token stride of %s is %lld: it must be 0 or in [%lld, 2^31]", name,
-                    (long long)stride, (long long)row);
-    return GDN_OK;
-}
-
-// One input of a call, for the copies: where the call reads its pointer, its row and stride.
-struct StridedIn {
-    const void** slot;
-    int64_t row, stride;
-    size_t es;
-};
-
-// Bytes of the dense copies of the strided inputs (each 256-byte aligned).
-size_t pack_bytes(const StridedIn* in, int n, size_t rows) {
-    size_t bytes = 0;
-    for (int i = 0; i < n; ++i)
-        if (*in[i].slot && strided(in[i].stride, in[i].row)) bytes += align256(rows * (size_t)in[i].row * in[i].es);
-    return bytes;
-}
-
-// Copies every strided input into `dst` (the workspace past the call's own part) and points its
-// slot at the copy.
-cudaError_t pack_inputs(const StridedIn* in, int n, size_t rows, char* dst, cudaStream_t st) {
-    for (int i = 0; i < n; ++i) {
-        if (!*in[i].slot || !strided(in[i].stride, in[i].row)) continue;
-        const long row_bytes = (long)(in[i].row * (int64_t)in[i].es);
-        cudaError_t e = pack_rows(*in[i].slot, dst, (long)rows, row_bytes, (long)(in[i].stride * (int64_t)in[i].es), st);
-        if (e != cudaSuccess) return e;
-        *in[i].slot = dst;
-        dst += align256(rows * (size_t)row_bytes);
-    }
-    return cudaSuccess;
 }
 
 // Gates as logits: the flag and alpha's per-head scale (grad: the scale's gradient, optional).
@@ -325,14 +244,6 @@ gdn_status check_bwd(const gdn_bwd_args* a) {
     return check_buffers(in, 12, out, 8);
 }
 
-gdn_status check_workspace(void* ws, size_t have, size_t need) {
-    if (need == 0) return GDN_OK;
-    if (!ws) return fail(GDN_ERR_WORKSPACE, "workspace is NULL, %zu bytes needed", need);
-    if (have < need) return fail(GDN_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", have, need);
-    if (reinterpret_cast<uintptr_t>(ws) & 255u) return fail(GDN_ERR_WORKSPACE, "workspace is not 256-byte aligned");
-    return GDN_OK;
-}
-
 ChunkIO io_from(const gdn_fwd_args* a) {
     ChunkIO io{};
     io.q = a->q; io.k = a->k; io.v = a->v; io.alpha = a->alpha; io.b = a->b; io.w = a->w;
@@ -386,9 +297,6 @@ size_t args_pack_bytes(const A* a) {
     const int n = LIST(&p, in);
     return pack_bytes(in, n, (size_t)(a->B * a->T));
 }
-// Workspace of a call's own part plus the copies of its strided inputs after it.
-size_t with_copies(size_t own, size_t copies) { return copies ? align256(own) + copies : own; }
-
 // Validates the workspace for a call's own part and its copies, then copies the strided inputs
 // of *a past its own part and points *a (the call's copy of its arguments) at them.
 template <class A>
@@ -404,9 +312,6 @@ gdn_status copy_strided(A* p, int (*list)(A*, StridedIn*), void* ws, size_t ws_b
     p->strides = gdn_strides{};
     return GDN_OK;
 }
-
-// Status word at the start of every workspace, cleared at the start of each call.
-int* ws_status(void* ws) { return static_cast<int*>(ws); }
 
 // The flag array of the pairs outside the chunk form's decay range, cleared at the start of a call.
 cudaError_t clear_flags(int* flags, const Problem& pb, cudaStream_t st) {

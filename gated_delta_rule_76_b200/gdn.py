@@ -7,6 +7,7 @@ device, the call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional, Tuple
@@ -83,11 +84,58 @@ class LayerBwdArgs(ctypes.Structure):
                 ("alpha_scale", P), ("grad_alpha_scale", P), ("strides", Strides)]
 
 
+class QkNorm(ctypes.Structure):
+    _fields_ = [("q_norm_w", P), ("k_norm_w", P), ("inv_freq", P), ("rot_dim", I64), ("interleaved", I32),
+                ("norm_eps", F32), ("rot_scale", F32)]
+
+
+class QkFwdArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("positions", P), ("q_out", P), ("k_out", P), ("T", I64), ("Hq", I64),
+                ("Hk", I64), ("d", I64), ("dtype", I32), ("norm", QkNorm), ("strides", Strides)]
+
+
+class QkBwdArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("positions", P), ("grad_q_out", P), ("grad_k_out", P), ("grad_q", P),
+                ("grad_k", P), ("grad_q_norm_w", P), ("grad_k_norm_w", P), ("T", I64), ("Hq", I64), ("Hk", I64),
+                ("d", I64), ("dtype", I32), ("norm", QkNorm), ("strides", Strides)]
+
+
+class AttnFwdArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("v", P), ("cu_seqlens", P), ("o", P), ("T", I64), ("nseq", I64), ("Hq", I64),
+                ("Hk", I64), ("d", I64), ("window", I64), ("scale", F32), ("dtype", I32), ("bwd_cache", P),
+                ("bwd_cache_bytes", ctypes.c_size_t), ("strides", Strides)]
+
+
+class AttnBwdArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("v", P), ("cu_seqlens", P), ("o", P), ("grad_o", P), ("grad_q", P),
+                ("grad_k", P), ("grad_v", P), ("T", I64), ("nseq", I64), ("Hq", I64), ("Hk", I64), ("d", I64),
+                ("window", I64), ("scale", F32), ("dtype", I32), ("fwd_cache", P),
+                ("fwd_cache_bytes", ctypes.c_size_t), ("strides", Strides)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k", P), ("v", P), ("cu_seqlens", P), ("context_lens", P), ("block_table", P),
+                ("q_out", P), ("k_out", P), ("k_cache", P), ("v_cache", P), ("T", I64), ("nseq", I64), ("Hq", I64),
+                ("Hk", I64), ("d", I64), ("num_pages", I64), ("page_size", I64), ("max_pages", I64),
+                ("dtype", I32), ("norm", QkNorm), ("strides", Strides)]
+
+
+class AttnDecodeArgs(ctypes.Structure):
+    _fields_ = [("q", P), ("k_cache", P), ("v_cache", P), ("block_table", P), ("context_lens", P), ("o", P),
+                ("N", I64), ("Hq", I64), ("Hk", I64), ("d", I64), ("num_pages", I64), ("page_size", I64),
+                ("max_pages", I64), ("max_context", I64), ("window", I64), ("scale", F32), ("dtype", I32),
+                ("strides", Strides)]
+
+
 EXPORTED = ["gdn_chunk_fwd_cache_size", "gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_noalloc",
             "gdn_chunk_fwd_noalloc_status", "gdn_chunk_bwd_workspace_size",
             "gdn_chunk_bwd", "gdn_decode_step", "gdn_layer_core_fwd_cache_size", "gdn_layer_core_fwd_workspace_size",
             "gdn_layer_core_fwd", "gdn_layer_core_bwd_workspace_size", "gdn_layer_core_bwd",
             "gdn_segment_map_workspace_size", "gdn_segment_map", "gdn_state_compose",
+            "gdn_qk_norm_rope_fwd", "gdn_qk_norm_rope_bwd_workspace_size", "gdn_qk_norm_rope_bwd",
+            "gdn_attn_fwd_cache_size", "gdn_attn_fwd_workspace_size", "gdn_attn_fwd",
+            "gdn_attn_bwd_workspace_size", "gdn_attn_bwd", "gdn_kv_append",
+            "gdn_attn_decode_workspace_size", "gdn_attn_decode",
             "gdn_workspace_status", "gdn_last_error", "gdn_kernel_launches", "gdn_version"]
 
 _lib = None
@@ -137,6 +185,19 @@ def load(path: str = LIB_PATH):
     lib.gdn_segment_map.restype = ctypes.c_int
     lib.gdn_state_compose.argtypes = [P, P, P, P, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32, P]
     lib.gdn_state_compose.restype = ctypes.c_int
+    lib.gdn_qk_norm_rope_fwd.argtypes = [ctypes.POINTER(QkFwdArgs), P]
+    lib.gdn_qk_norm_rope_fwd.restype = ctypes.c_int
+    lib.gdn_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), P]
+    lib.gdn_kv_append.restype = ctypes.c_int
+    for name, struct in (("gdn_qk_norm_rope_bwd", QkBwdArgs), ("gdn_attn_fwd", AttnFwdArgs),
+                         ("gdn_attn_bwd", AttnBwdArgs), ("gdn_attn_decode", AttnDecodeArgs)):
+        size, call = getattr(lib, name + "_workspace_size"), getattr(lib, name)
+        size.argtypes = [ctypes.POINTER(struct)]
+        size.restype = ctypes.c_size_t
+        call.argtypes = [ctypes.POINTER(struct), P, ctypes.c_size_t, P]
+        call.restype = ctypes.c_int
+    lib.gdn_attn_fwd_cache_size.argtypes = [ctypes.POINTER(AttnFwdArgs)]
+    lib.gdn_attn_fwd_cache_size.restype = ctypes.c_size_t
     lib.gdn_workspace_status.argtypes = [P, P]
     lib.gdn_workspace_status.restype = ctypes.c_int
     lib.gdn_last_error.argtypes = []
@@ -557,3 +618,290 @@ def gdn_layer_core_bwd(xq, xk, xv, conv_w, alpha, z, grad_y, b=None, w=None, bet
     ws = _workspace(need, dev, workspace)
     check(lib.gdn_layer_core_bwd(ctypes.byref(a), _ptr(ws), need, _stream(stream)), "gdn_layer_core_bwd")
     return out
+
+
+# ---------------------------------------------------------------------------------------------
+# the softmax-attention layer of hybrid stacks
+# ---------------------------------------------------------------------------------------------
+_AS_IS = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, stream):
+    """The context the calls below run in: their tensors' device, whichever is current, and the given
+    stream, so that what they allocate (results, workspace) belongs to the stream they run on."""
+    if not t.is_cuda:
+        raise GdnError("libgdn takes CUDA tensors only (there is no CPU path)")
+    if stream is None:
+        return _AS_IS if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    return torch.cuda.stream(stream)
+
+
+def _same_device(ref: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise GdnError(f"{name} is on {t.device}, not on {ref.device}")
+
+
+def _same_dtype(ref: torch.Tensor, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != ref.dtype:
+            raise GdnError(f"{name} has dtype {t.dtype}, expected {ref.dtype}")
+
+
+def _shape(name: str, t: Optional[torch.Tensor], shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise GdnError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _i32(name: str, t: Optional[torch.Tensor]):
+    if t is not None and t.dtype != torch.int32:
+        raise GdnError(f"{name} has dtype {t.dtype}, expected torch.int32")
+
+
+def _cu_seqlens(cu, device, T: int):
+    """cu_seqlens as an int32 device array.  One given on the host (a list or a CPU tensor) is checked
+    before it is uploaded; one on the device is passed through (checking it would synchronise)."""
+    if cu is None:
+        return None
+    if not torch.is_tensor(cu):
+        cu = torch.tensor(cu, dtype=torch.int64)
+    if cu.dim() != 1 or cu.numel() < 1:
+        raise GdnError("cu_seqlens needs nseq + 1 entries")
+    if cu.device.type == "cpu":
+        x = cu.tolist()
+        if any(b < a for a, b in zip(x, x[1:])) or x[0] < 0 or x[-1] > T:
+            raise GdnError(f"cu_seqlens must ascend from >= 0 to <= {T} tokens")
+        return cu.to(device=device, dtype=torch.int32)
+    _i32("cu_seqlens", cu)
+    return cu.contiguous()
+
+
+def _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale) -> QkNorm:
+    ref = q if q is not None else k
+    for name, w in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
+        _shape(name, w, (ref.shape[-1],))
+    _same_dtype(ref, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
+    if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1):
+        raise GdnError("inv_freq is a vector of fp32 frequencies")
+    return QkNorm(q_norm_w=_ptr(q_norm_w), k_norm_w=_ptr(k_norm_w), inv_freq=_ptr(inv_freq),
+                  rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(), interleaved=int(interleaved),
+                  norm_eps=norm_eps, rot_scale=rot_scale)
+
+
+def _packed(name: str, t: torch.Tensor, T: Optional[int] = None, d: Optional[int] = None):
+    if t.dim() != 3 or (T is not None and t.shape[0] != T) or (d is not None and t.shape[2] != d):
+        raise GdnError(f"{name} has shape {tuple(t.shape)}: expected [{T if T is not None else 'T'}, heads, "
+                       f"{d if d is not None else 'd'}]")
+
+
+def _qk_args(cls, q, k, positions, norm, **more):
+    _packed("q", q)
+    T, Hq, d = q.shape
+    if k is not None:
+        _packed("k", k, T, d)
+        _same_dtype(q, k=k)
+    _i32("positions", positions)
+    _shape("positions", positions, (T,))
+    (pq, sq), (pk, sk) = _tok(q, 1), _tok(k, 1)
+    return cls(q=pq, k=pk, positions=_ptr(positions), T=T, Hq=Hq, Hk=0 if k is None else k.shape[1], d=d,
+               dtype=_dt(q), norm=norm, strides=Strides(q=sq, k=sk), **more)
+
+
+def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, k_norm_w=None,
+                         norm_eps: float = NORM_EPS, interleaved: bool = False, rot_scale: float = 1.0,
+                         q_out=None, k_out=None, stream=None):
+    """Per-head RMS norm of q [T,Hq,d] and k [T,Hk,d] (or None) and the rotation of their first
+    ``2 * len(inv_freq)`` channels by ``positions`` [T] int32.  Returns (q_out, k_out)."""
+    with _on(q, stream):
+        _same_device(q, k=k, positions=positions, inv_freq=inv_freq, q_norm_w=q_norm_w, k_norm_w=k_norm_w,
+                     q_out=q_out, k_out=k_out)
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if k_out is None and k is not None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _shape("q_out", q_out, q.shape)
+        _same_dtype(q, q_out=q_out, k_out=k_out)
+        if k is not None:
+            _shape("k_out", k_out, k.shape)
+        norm = _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
+        a = _qk_args(QkFwdArgs, q, k, positions, norm, q_out=_ptr(q_out), k_out=_ptr(k_out))
+        check(load().gdn_qk_norm_rope_fwd(ctypes.byref(a), _stream(None)), "gdn_qk_norm_rope_fwd")
+    return q_out, k_out
+
+
+def gdn_qk_norm_rope_bwd(q, k, positions=None, inv_freq=None, *, grad_q, grad_k=None, q_norm_w=None, k_norm_w=None,
+                         norm_eps: float = NORM_EPS, interleaved: bool = False, rot_scale: float = 1.0,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
+    """Reverse mode of gdn_qk_norm_rope_fwd for the gradients ``grad_q``, ``grad_k`` of its results.
+    Returns dq, dk in the inputs' dtype and dq_norm_w, dk_norm_w [d] fp32 (those that apply)."""
+    with _on(q, stream):
+        _same_device(q, k=k, positions=positions, inv_freq=inv_freq, q_norm_w=q_norm_w, k_norm_w=k_norm_w,
+                     grad_q=grad_q, grad_k=grad_k, workspace=workspace)
+        _shape("grad_q", grad_q, q.shape)
+        _same_dtype(q, grad_q=grad_q, grad_k=grad_k)
+        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device)}
+        if k is not None:
+            if grad_k is None:
+                raise GdnError("grad_k is required with k")
+            _shape("grad_k", grad_k, k.shape)
+            out["dk"] = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        for name, w in (("dq_norm_w", q_norm_w), ("dk_norm_w", k_norm_w)):
+            if w is not None:
+                out[name] = torch.empty(w.shape, dtype=torch.float32, device=q.device)
+        norm = _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
+        a = _qk_args(QkBwdArgs, q, k, positions, norm, grad_q_out=_ptr(grad_q), grad_k_out=_ptr(grad_k),
+                     grad_q=_ptr(out["dq"]), grad_k=_ptr(out.get("dk")), grad_q_norm_w=_ptr(out.get("dq_norm_w")),
+                     grad_k_norm_w=_ptr(out.get("dk_norm_w")))
+        lib = load()
+        need = lib.gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(a))
+        ws = _workspace(need, q.device, workspace)
+        check(lib.gdn_qk_norm_rope_bwd(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_qk_norm_rope_bwd")
+    return out
+
+
+def _attn_args(cls, q, k, v, cu, scale, window, **more):
+    _packed("q", q)
+    T, Hq, d = q.shape
+    _packed("k", k, T, d)
+    _shape("v", v, k.shape)
+    _same_dtype(q, k=k, v=v)
+    (pq, sq), (pk, sk), (pv, sv) = _tok(q, 1), _tok(k, 1), _tok(v, 1)
+    return cls(q=pq, k=pk, v=pv, cu_seqlens=_ptr(cu), T=T, nseq=cu.numel() - 1, Hq=Hq, Hk=k.shape[1], d=d,
+               window=window, scale=d ** -0.5 if scale is None else scale, dtype=_dt(q),
+               strides=Strides(q=sq, k=sk, v=sv), **more)
+
+
+def gdn_attn_fwd_cache_size(q, k, v, cu_seqlens) -> int:
+    """Bytes of the cache gdn_attn_fwd(..., bwd_cache=) fills for gdn_attn_bwd."""
+    cu = _cu_seqlens(cu_seqlens, q.device, q.shape[0])
+    return int(load().gdn_attn_fwd_cache_size(ctypes.byref(_attn_args(AttnFwdArgs, q, k, v, cu, None, 0))))
+
+
+def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: int = 0, o=None,
+                 bwd_cache: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention over packed sequences: q [T,Hq,d], k and v [T,Hk,d] bf16, ``cu_seqlens``
+    [nseq + 1] (int32 on the device, or a list or CPU tensor, which is checked).  ``scale``: d ** -0.5
+    unless given; ``window``: 0, or how many tokens, itself included, a token sees.  Returns o; rows
+    outside every sequence stay as they were (unset in an ``o`` made here)."""
+    with _on(q, stream):
+        _same_device(q, k=k, v=v, o=o, bwd_cache=bwd_cache, workspace=workspace)
+        cu = _cu_seqlens(cu_seqlens, q.device, q.shape[0])
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _shape("o", o, q.shape)
+        _same_dtype(q, o=o)
+        a = _attn_args(AttnFwdArgs, q, k, v, cu, scale, window, o=_ptr(o), bwd_cache=_ptr(bwd_cache),
+                       bwd_cache_bytes=0 if bwd_cache is None else bwd_cache.numel() * bwd_cache.element_size())
+        lib = load()
+        need = lib.gdn_attn_fwd_workspace_size(ctypes.byref(a))
+        ws = _workspace(need, q.device, workspace)
+        check(lib.gdn_attn_fwd(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_attn_fwd")
+    return o
+
+
+def gdn_attn_bwd(q, k, v, cu_seqlens, o, *, grad_o, fwd_cache: torch.Tensor, scale: Optional[float] = None,
+                 window: int = 0, dq=None, dk=None, dv=None, workspace: Optional[torch.Tensor] = None,
+                 stream=None) -> Dict[str, torch.Tensor]:
+    """Reverse mode of gdn_attn_fwd from its output ``o`` and the cache it filled.  Returns dq, dk, dv
+    in bf16 (``dq``, ``dk``, ``dv``: buffers to fill; rows outside every sequence stay as they were)."""
+    with _on(q, stream):
+        _same_device(q, k=k, v=v, o=o, grad_o=grad_o, fwd_cache=fwd_cache, dq=dq, dk=dk, dv=dv, workspace=workspace)
+        cu = _cu_seqlens(cu_seqlens, q.device, q.shape[0])
+        like = lambda t, given: torch.empty(t.shape, dtype=t.dtype, device=t.device) if given is None else given
+        out = {"dq": like(q, dq), "dk": like(k, dk), "dv": like(v, dv)}
+        for name, t, ref in (("o", o, q), ("grad_o", grad_o, q), ("dq", out["dq"], q), ("dk", out["dk"], k),
+                             ("dv", out["dv"], k)):
+            _shape(name, t, ref.shape)
+            _same_dtype(q, **{name: t})
+        a = _attn_args(AttnBwdArgs, q, k, v, cu, scale, window, o=_ptr(o), grad_o=_ptr(grad_o),
+                       grad_q=_ptr(out["dq"]), grad_k=_ptr(out["dk"]), grad_v=_ptr(out["dv"]),
+                       fwd_cache=_ptr(fwd_cache), fwd_cache_bytes=fwd_cache.numel() * fwd_cache.element_size())
+        lib = load()
+        need = lib.gdn_attn_bwd_workspace_size(ctypes.byref(a))
+        ws = _workspace(need, q.device, workspace)
+        check(lib.gdn_attn_bwd(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_attn_bwd")
+    return out
+
+
+def _cache_dims(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, dtype):
+    """(num_pages, page_size, max_pages) of a paged cache [num_pages, page_size, Hk, d]."""
+    if k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (Hk, d):
+        raise GdnError(f"k_cache has shape {tuple(k_cache.shape)}: expected [num_pages, page_size, {Hk}, {d}]")
+    _shape("v_cache", v_cache, k_cache.shape)
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise GdnError(f"the caches have dtypes {k_cache.dtype}, {v_cache.dtype}, expected {dtype}")
+    _i32("block_table", block_table)
+    _i32("context_lens", context_lens)
+    if block_table.dim() != 2 or block_table.shape[0] != nseq:
+        raise GdnError(f"block_table has shape {tuple(block_table.shape)}: expected [{nseq}, max_pages]")
+    _shape("context_lens", context_lens, (nseq,))
+    return k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+
+
+def gdn_kv_append(k, v, k_cache, v_cache, block_table, context_lens, *, cu_seqlens=None, q=None, inv_freq=None,
+                  q_norm_w=None, k_norm_w=None, norm_eps: float = NORM_EPS, interleaved: bool = False,
+                  rot_scale: float = 1.0, q_out=None, k_out=None, want_k: bool = False, stream=None):
+    """Appends the new tokens' k (normalised and rotated at its cache position) and v [T,Hk,d] to the
+    paged caches [num_pages, page_size, Hk, d], in place.  ``context_lens`` [nseq] int32: tokens cached
+    before (unchanged); ``cu_seqlens``: the sequences' new tokens, None for one each.  With ``q``
+    [T,Hq,d], the same norm and rotation of q.  Returns (q_out or None, k_out or None: the keys as
+    cached, with ``want_k``)."""
+    with _on(k, stream):
+        _same_device(k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens, q=q,
+                     inv_freq=inv_freq, q_norm_w=q_norm_w, k_norm_w=k_norm_w, q_out=q_out, k_out=k_out)
+        _packed("k", k)
+        T, Hk, d = k.shape
+        _shape("v", v, k.shape)
+        _same_dtype(k, v=v, q=q, q_out=q_out, k_out=k_out)
+        cu = _cu_seqlens(cu_seqlens, k.device, T)
+        nseq = T if cu is None else cu.numel() - 1
+        pages, page, most = _cache_dims(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, k.dtype)
+        if q is not None:
+            _packed("q", q, T, d)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            _shape("q_out", q_out, q.shape)
+        elif q_out is not None:
+            raise GdnError("q_out needs q")
+        if want_k and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+        _shape("k_out", k_out, k.shape)
+        norm = _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
+        (pq, sq), (pk, sk), (pv, sv) = _tok(q, 1), _tok(k, 1), _tok(v, 1)
+        a = KvAppendArgs(q=pq, k=pk, v=pv, cu_seqlens=_ptr(cu), context_lens=_ptr(context_lens),
+                         block_table=_ptr(block_table), q_out=_ptr(q_out), k_out=_ptr(k_out), k_cache=_ptr(k_cache),
+                         v_cache=_ptr(v_cache), T=T, nseq=nseq, Hq=0 if q is None else q.shape[1], Hk=Hk, d=d,
+                         num_pages=pages, page_size=page, max_pages=most, dtype=_dt(k), norm=norm,
+                         strides=Strides(q=sq, k=sk, v=sv))
+        check(load().gdn_kv_append(ctypes.byref(a), _stream(None)), "gdn_kv_append")
+    return q_out, k_out
+
+
+def gdn_attn_decode(q, k_cache, v_cache, block_table, context_lens, *, scale: Optional[float] = None, window: int = 0,
+                    max_context: int = 0, o=None, workspace: Optional[torch.Tensor] = None, stream=None):
+    """One query token for N sequences, q [N,Hq,d], over the paged caches: ``context_lens`` [N] int32
+    tokens each, this one's included.  ``max_context``: a bound on the lengths that the caller knows
+    (0: the block table's reach).  Returns o [N,Hq,d]."""
+    with _on(q, stream):
+        _same_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens, o=o,
+                     workspace=workspace)
+        _packed("q", q)
+        N, Hq, d = q.shape
+        Hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
+        pages, page, most = _cache_dims(k_cache, v_cache, block_table, context_lens, N, Hk, d, q.dtype)
+        if o is None:
+            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        _shape("o", o, q.shape)
+        _same_dtype(q, o=o)
+        pq, sq = _tok(q, 1)
+        a = AttnDecodeArgs(q=pq, k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), block_table=_ptr(block_table),
+                           context_lens=_ptr(context_lens), o=_ptr(o), N=N, Hq=Hq, Hk=Hk, d=d, num_pages=pages,
+                           page_size=page, max_pages=most, max_context=max_context, window=window,
+                           scale=d ** -0.5 if scale is None else scale, dtype=_dt(q), strides=Strides(q=sq))
+        lib = load()
+        need = lib.gdn_attn_decode_workspace_size(ctypes.byref(a))
+        ws = _workspace(need, q.device, workspace)
+        check(lib.gdn_attn_decode(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_attn_decode")
+    return o

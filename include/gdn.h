@@ -432,6 +432,182 @@ GDN_API size_t gdn_layer_core_bwd_workspace_size(const gdn_layer_bwd_args* args)
 GDN_API gdn_status gdn_layer_core_bwd(const gdn_layer_bwd_args* args, void* workspace, size_t workspace_bytes,
                                       gdn_stream stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The softmax-attention layer of hybrid stacks.  Hybrids alternate gated-delta-rule layers with
+ * softmax attention, full or over a sliding window (explainer «Architecture et versions
+ * hybrides»: the H1 and H2 hybrids with a 2K window; the mkdocs chapter's production model is a
+ * hybrid too).  The calls below are that layer's core in the passes the recurrence has: the
+ * preparation of q and k, forward, backward, and the single-token step with its cache.
+ *
+ * Shared conventions, besides those at the top of this file:
+ *  - Packed tokens: q [T,Hq,d], k and v [T,Hk,d], T tokens of all sequences back to back.
+ *    cu_seqlens [nseq + 1] int32 on the device: sequence s is tokens cu_seqlens[s] ..
+ *    cu_seqlens[s + 1] - 1 (possibly none).  Tokens outside every sequence are neither read as keys
+ *    nor written: their outputs and gradients stay as they were.  The host cannot check the array;
+ *    kernels clamp its entries to [0, T] and to ascending order, and the results are then
+ *    unspecified.
+ *  - Grouped heads: query head h reads key head h / (Hq / Hk); Hq must be a multiple of Hk.
+ *  - d in {64, 128}; a window of w > 0 lets token i see tokens i - w + 1 .. i, 0 all of 0 .. i.
+ *  - gdn_strides: the fields q, k, v (the others must be 0).
+ * ------------------------------------------------------------------------------------------ */
+
+/* Per-head norm and rotation of q and k, shared by the two calls that take it.  For every head row
+ * x of d values at position p:
+ *     n = x / sqrt(mean_j x_j^2 + norm_eps) .* w        (w = q_norm_w or k_norm_w; NULL: n = x)
+ *     (y_a, y_b) = rot_scale * (n_a cos - n_b sin, n_b cos + n_a sin),  angle p * inv_freq[i]
+ * for pair i of the first rot_dim channels: (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) with
+ * interleaved = 1.  The other channels of y are n.  Positions scaled for long contexts are a matter
+ * of inv_freq and rot_scale, which the caller chooses.  Angles are reduced in 64 bits, so that far
+ * positions keep their precision; positions are exact up to 2^31 - 1. */
+typedef struct gdn_qk_norm {
+    const void* q_norm_w;  /* [d] dtype, or NULL: q is not normalised */
+    const void* k_norm_w;  /* [d] dtype, or NULL: k is not normalised */
+    const float* inv_freq; /* [rot_dim / 2] fp32; NULL exactly when rot_dim = 0 */
+    int64_t rot_dim;       /* rotated channels, a multiple of 16, at most d; 0: no rotation */
+    int32_t interleaved;   /* 0: halves, 1: neighbouring channels */
+    float norm_eps;        /* >= 0 */
+    float rot_scale;       /* factor on cos and sin (1 = a plain rotation) */
+} gdn_qk_norm;
+
+/* Norm and rotation of packed q and k, and its reverse mode.  dtype BF16 or F32; every result is
+ * rounded once from fp32.  k may be NULL with Hk = 0 (q alone). */
+typedef struct gdn_qk_fwd_args {
+    const void* q;              /* [T,Hq,d] dtype */
+    const void* k;              /* [T,Hk,d] dtype */
+    const int32_t* positions;   /* [T]; NULL exactly when rot_dim = 0 */
+    void* q_out;                /* out [T,Hq,d] dtype */
+    void* k_out;                /* out [T,Hk,d] dtype */
+    int64_t T, Hq, Hk, d;
+    int32_t dtype;
+    gdn_qk_norm norm;
+    gdn_strides strides;        /* q, k (read in place) */
+} gdn_qk_fwd_args;
+
+GDN_API gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_fwd_args* args, gdn_stream stream);
+
+typedef struct gdn_qk_bwd_args {
+    const void* q;              /* the forward's inputs */
+    const void* k;
+    const int32_t* positions;
+    const void* grad_q_out;     /* [T,Hq,d] dtype, dense */
+    const void* grad_k_out;     /* [T,Hk,d] dtype, dense */
+    void* grad_q;               /* out [T,Hq,d] dtype */
+    void* grad_k;               /* out [T,Hk,d] dtype */
+    float* grad_q_norm_w;       /* out [d] fp32, required exactly with q_norm_w: summed over tokens and heads in a */
+    float* grad_k_norm_w;       /* fixed order on a given GPU; the same for k */
+    int64_t T, Hq, Hk, d;
+    int32_t dtype;
+    gdn_qk_norm norm;
+    gdn_strides strides;        /* q, k (read in place) */
+} gdn_qk_bwd_args;
+
+GDN_API size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_bwd_args* args);
+GDN_API gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_bwd_args* args, void* workspace, size_t workspace_bytes,
+                                        gdn_stream stream);
+
+/* Causal softmax attention over packed sequences, forward:
+ *     s_ij = scale q_i . k_j  for j <= i (and j > i - window),   o_i = sum_j softmax_j(s_ij) v_j
+ * with i, j the tokens of one sequence.  bf16 only (GDN_ERR_UNSUPPORTED otherwise).  Within a
+ * sequence the values must be finite: a NaN or infinity in one token's k or v can reach any
+ * output of its sequence, but none of another one.  The workspace starts with the status word that
+ * gdn_workspace_status reads.  A strided q, k or v whose address and stride are multiples of 16
+ * bytes is read in place, any other strided one from a dense copy in the workspace. */
+typedef struct gdn_attn_fwd_args {
+    const void* q;              /* [T,Hq,d] dtype */
+    const void* k;              /* [T,Hk,d] dtype */
+    const void* v;              /* [T,Hk,d] dtype */
+    const int32_t* cu_seqlens;  /* [nseq + 1] */
+    void* o;                    /* out [T,Hq,d] dtype */
+    int64_t T, nseq, Hq, Hk, d, window;
+    float scale;
+    int32_t dtype;              /* GDN_BF16 */
+    /* Optional cache for gdn_attn_bwd over the same inputs: gdn_attn_fwd_cache_size(args) bytes, 256-byte
+     * aligned.  It receives each row's log-sum-exp and what o's rounding left out. */
+    void* bwd_cache;
+    size_t bwd_cache_bytes;
+    gdn_strides strides;        /* q, k, v */
+} gdn_attn_fwd_args;
+
+GDN_API size_t gdn_attn_fwd_cache_size(const gdn_attn_fwd_args* args);
+GDN_API size_t gdn_attn_fwd_workspace_size(const gdn_attn_fwd_args* args);
+GDN_API gdn_status gdn_attn_fwd(const gdn_attn_fwd_args* args, void* workspace, size_t workspace_bytes,
+                                gdn_stream stream);
+
+/* Its reverse mode.  Gradients are returned in bf16, each rounded once from fp32; those of k and v are
+ * summed in fp32 over the query heads that share a key head, in a fixed order. */
+typedef struct gdn_attn_bwd_args {
+    const void* q;              /* the forward's inputs */
+    const void* k;
+    const void* v;
+    const int32_t* cu_seqlens;
+    const void* o;              /* [T,Hq,d] dtype: the forward's output */
+    const void* grad_o;         /* [T,Hq,d] dtype, dense */
+    void* grad_q;               /* out [T,Hq,d] dtype */
+    void* grad_k;               /* out [T,Hk,d] dtype */
+    void* grad_v;               /* out [T,Hk,d] dtype */
+    int64_t T, nseq, Hq, Hk, d, window;
+    float scale;
+    int32_t dtype;
+    const void* fwd_cache;      /* required: what a gdn_attn_fwd call over exactly these inputs wrote; the library
+                                 * cannot check that it did */
+    size_t fwd_cache_bytes;
+    gdn_strides strides;        /* q, k, v */
+} gdn_attn_bwd_args;
+
+GDN_API size_t gdn_attn_bwd_workspace_size(const gdn_attn_bwd_args* args);
+GDN_API gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* args, void* workspace, size_t workspace_bytes,
+                                gdn_stream stream);
+
+/* Paged cache of keys and values: k_cache, v_cache [num_pages,page_size,Hk,d] bf16; token p of
+ * sequence s lives in page block_table[s][p / page_size], slot p % page_size.  Pages outside [0, num_pages)
+ * and positions past the table are neither read nor written.
+ *
+ * gdn_kv_append: the new tokens' k, normalised and rotated at their cache position, and v into the cache;
+ * with q, the same tokens' q, normalised and rotated, into q_out.  Token i of sequence s takes position
+ * context_lens[s] + i, context_lens being the tokens cached before (the call does not change it).
+ * cu_seqlens NULL: one new token a sequence (T = nseq).  Two tokens sent to one slot leave either there.
+ * Tokens outside every sequence are left out. */
+typedef struct gdn_kv_append_args {
+    const void* q;              /* [T,Hq,d] dtype, or NULL (then Hq = 0) */
+    const void* k;              /* [T,Hk,d] dtype */
+    const void* v;              /* [T,Hk,d] dtype */
+    const int32_t* cu_seqlens;  /* [nseq + 1], or NULL */
+    const int32_t* context_lens; /* [nseq] */
+    const int32_t* block_table; /* [nseq,max_pages] */
+    void* q_out;                /* out [T,Hq,d] dtype, with q */
+    void* k_out;                /* out [T,Hk,d] dtype: the keys as cached, may be NULL */
+    void* k_cache;              /* in/out */
+    void* v_cache;              /* in/out */
+    int64_t T, nseq, Hq, Hk, d, num_pages, page_size, max_pages;
+    int32_t dtype;              /* GDN_BF16 */
+    gdn_qk_norm norm;
+    gdn_strides strides;        /* q, k, v (read in place) */
+} gdn_kv_append_args;
+
+GDN_API gdn_status gdn_kv_append(const gdn_kv_append_args* args, gdn_stream stream);
+
+/* One query token a sequence over the paged cache: o_n = sum_j softmax_j(scale q_n . k_j) v_j over the
+ * context_lens[n] cached tokens (with a window, the last `window` of them).  A sequence whose length is 0,
+ * or whose every page is out of range, gets o = 0.  max_context bounds the lengths (longer ones are read as
+ * max_context) and sets how the work is split; 0: max_pages * page_size.  The partial results of a split
+ * context are joined in a fixed order. */
+typedef struct gdn_attn_decode_args {
+    const void* q;              /* [N,Hq,d] dtype */
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_table; /* [N,max_pages] */
+    const int32_t* context_lens; /* [N] */
+    void* o;                    /* out [N,Hq,d] dtype */
+    int64_t N, Hq, Hk, d, num_pages, page_size, max_pages, max_context, window;
+    float scale;
+    int32_t dtype;              /* GDN_BF16 */
+    gdn_strides strides;        /* q (per sequence, read in place) */
+} gdn_attn_decode_args;
+
+GDN_API size_t gdn_attn_decode_workspace_size(const gdn_attn_decode_args* args);
+GDN_API gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* workspace, size_t workspace_bytes,
+                                   gdn_stream stream);
+
 /* Device-side status of the last call that used `workspace` (a chunk forward, backward or layer
  * core).  The tensor-core kernels bound every internal wait; when one expires the kernel records
  * it in the workspace, stops issuing work, releases its tensor memory and returns.  This call
