@@ -622,6 +622,9 @@ def gdn_layer_core_bwd(xq, xk, xv, conv_w, alpha, z, grad_y, b=None, w=None, bet
 
 # ---------------------------------------------------------------------------------------------
 # the softmax-attention layer of hybrid stacks
+#
+# Serving calls these once a token and layer, on kernels of a few microseconds: the marshalling below
+# keeps to plain comparisons, and builds its structs from positional values.
 # ---------------------------------------------------------------------------------------------
 _AS_IS = contextlib.nullcontext()
 
@@ -632,81 +635,83 @@ def _on(t: torch.Tensor, stream):
     if not t.is_cuda:
         raise GdnError("libgdn takes CUDA tensors only (there is no CPU path)")
     if stream is None:
-        return _AS_IS if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+        return _AS_IS if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     return torch.cuda.stream(stream)
 
 
-def _same_device(ref: torch.Tensor, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise GdnError(f"{name} is on {t.device}, not on {ref.device}")
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _same_dtype(ref: torch.Tensor, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != ref.dtype:
-            raise GdnError(f"{name} has dtype {t.dtype}, expected {ref.dtype}")
-
-
-def _shape(name: str, t: Optional[torch.Tensor], shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
-        raise GdnError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-
-
-def _i32(name: str, t: Optional[torch.Tensor]):
-    if t is not None and t.dtype != torch.int32:
-        raise GdnError(f"{name} has dtype {t.dtype}, expected torch.int32")
-
-
-def _cu_seqlens(cu, device, T: int):
-    """cu_seqlens as an int32 device array.  One given on the host (a list or a CPU tensor) is checked
-    before it is uploaded; one on the device is passed through (checking it would synchronise)."""
-    if cu is None:
+def _dense(name: str, t: Optional[torch.Tensor], shape, dtype, device: int):
+    """The address of a contiguous tensor of this shape (None: any), dtype and device, or None."""
+    if t is None:
         return None
+    if (shape is not None and t.shape != shape) or t.dtype != dtype or t.get_device() != device:
+        raise GdnError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}: expected "
+                       f"{'' if shape is None else tuple(shape)} {dtype} on cuda:{device}")
+    if not t.is_contiguous():
+        raise GdnError("libgdn takes contiguous tensors")
+    return t.data_ptr()
+
+
+def _packed(name: str, t: torch.Tensor, shape, dtype, device: int):
+    """(address, token stride) of packed tokens [T, heads, d]; shape: what is known of it (-1: any)."""
+    if t.dim() != 3 or any(n not in (-1, m) for n, m in zip(shape, t.shape)) or t.dtype != dtype or t.get_device() != device:
+        raise GdnError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}: expected {tuple(shape)} {dtype} on cuda:{device}")
+    if t.is_contiguous():
+        return t.data_ptr(), 0
+    return t.data_ptr(), _token_stride(t.shape, t.stride(), 1)
+
+
+def _bytes(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor]):
+    """(address, the tensor that holds it) of a workspace of nbytes: the caller's where it is large enough."""
+    if nbytes == 0:
+        return None, None
+    if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
+        workspace = like.new_empty((nbytes,), dtype=torch.uint8)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise GdnError(f"the workspace must be contiguous and on {like.device}")
+    return workspace.data_ptr(), workspace
+
+
+def _cu_seqlens(cu, device: int, T: int):
+    """cu_seqlens as (address, number of sequences, the int32 device array).  One given on the host (a
+    list or a CPU tensor) is checked before it is uploaded; one on the device is passed through
+    (checking it would synchronise)."""
     if not torch.is_tensor(cu):
         cu = torch.tensor(cu, dtype=torch.int64)
     if cu.dim() != 1 or cu.numel() < 1:
         raise GdnError("cu_seqlens needs nseq + 1 entries")
-    if cu.device.type == "cpu":
+    if not cu.is_cuda:
         x = cu.tolist()
         if any(b < a for a, b in zip(x, x[1:])) or x[0] < 0 or x[-1] > T:
             raise GdnError(f"cu_seqlens must ascend from >= 0 to <= {T} tokens")
-        return cu.to(device=device, dtype=torch.int32)
-    _i32("cu_seqlens", cu)
-    return cu.contiguous()
+        cu = cu.to(device=f"cuda:{device}", dtype=torch.int32)
+    return _dense("cu_seqlens", cu, None, torch.int32, device), cu.numel() - 1, cu
 
 
-def _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale) -> QkNorm:
-    ref = q if q is not None else k
-    for name, w in (("q_norm_w", q_norm_w), ("k_norm_w", k_norm_w)):
-        _shape(name, w, (ref.shape[-1],))
-    _same_dtype(ref, q_norm_w=q_norm_w, k_norm_w=k_norm_w)
-    if inv_freq is not None and (inv_freq.dtype != torch.float32 or inv_freq.dim() != 1):
-        raise GdnError("inv_freq is a vector of fp32 frequencies")
-    return QkNorm(q_norm_w=_ptr(q_norm_w), k_norm_w=_ptr(k_norm_w), inv_freq=_ptr(inv_freq),
-                  rot_dim=0 if inv_freq is None else 2 * inv_freq.numel(), interleaved=int(interleaved),
-                  norm_eps=norm_eps, rot_scale=rot_scale)
+def _qk_norm(d, dtype, device, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale) -> QkNorm:
+    rot = 0
+    if inv_freq is not None:
+        if inv_freq.dim() != 1:
+            raise GdnError("inv_freq is a vector of fp32 frequencies")
+        rot = 2 * inv_freq.numel()
+    return QkNorm(_dense("q_norm_w", q_norm_w, (d,), dtype, device), _dense("k_norm_w", k_norm_w, (d,), dtype, device),
+                  _dense("inv_freq", inv_freq, None, torch.float32, device), rot, int(interleaved), norm_eps, rot_scale)
 
 
-def _packed(name: str, t: torch.Tensor, T: Optional[int] = None, d: Optional[int] = None):
-    if t.dim() != 3 or (T is not None and t.shape[0] != T) or (d is not None and t.shape[2] != d):
-        raise GdnError(f"{name} has shape {tuple(t.shape)}: expected [{T if T is not None else 'T'}, heads, "
-                       f"{d if d is not None else 'd'}]")
-
-
-def _qk_args(cls, q, k, positions, norm, **more):
-    _packed("q", q)
+def _qk_inputs(q, k):
+    """(device, dtype, T, Hq, Hk, d, q's address, k's, Strides) of packed q and k (or None)."""
+    dev, dtype = q.get_device(), q.dtype
+    pq, sq = _packed("q", q, (-1, -1, -1), dtype, dev)
     T, Hq, d = q.shape
-    if k is not None:
-        _packed("k", k, T, d)
-        _same_dtype(q, k=k)
-    _i32("positions", positions)
-    _shape("positions", positions, (T,))
-    (pq, sq), (pk, sk) = _tok(q, 1), _tok(k, 1)
-    return cls(q=pq, k=pk, positions=_ptr(positions), T=T, Hq=Hq, Hk=0 if k is None else k.shape[1], d=d,
-               dtype=_dt(q), norm=norm, strides=Strides(q=sq, k=sk), **more)
+    if k is None:
+        return dev, dtype, T, Hq, 0, d, pq, None, Strides(sq)
+    pk, sk = _packed("k", k, (T, -1, d), dtype, dev)
+    return dev, dtype, T, Hq, k.shape[1], d, pq, pk, Strides(sq, sk)
 
 
 def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, k_norm_w=None,
@@ -715,19 +720,16 @@ def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, 
     """Per-head RMS norm of q [T,Hq,d] and k [T,Hk,d] (or None) and the rotation of their first
     ``2 * len(inv_freq)`` channels by ``positions`` [T] int32.  Returns (q_out, k_out)."""
     with _on(q, stream):
-        _same_device(q, k=k, positions=positions, inv_freq=inv_freq, q_norm_w=q_norm_w, k_norm_w=k_norm_w,
-                     q_out=q_out, k_out=k_out)
+        dev, dtype, T, Hq, Hk, d, pq, pk, strides = _qk_inputs(q, k)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = q.new_empty(q.shape)
         if k_out is None and k is not None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _shape("q_out", q_out, q.shape)
-        _same_dtype(q, q_out=q_out, k_out=k_out)
-        if k is not None:
-            _shape("k_out", k_out, k.shape)
-        norm = _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
-        a = _qk_args(QkFwdArgs, q, k, positions, norm, q_out=_ptr(q_out), k_out=_ptr(k_out))
-        check(load().gdn_qk_norm_rope_fwd(ctypes.byref(a), _stream(None)), "gdn_qk_norm_rope_fwd")
+            k_out = k.new_empty(k.shape)
+        a = QkFwdArgs(pq, pk, _dense("positions", positions, (T,), torch.int32, dev),
+                      _dense("q_out", q_out, q.shape, dtype, dev),
+                      _dense("k_out", k_out, None if k is None else k.shape, dtype, dev), T, Hq, Hk, d, _dt(q),
+                      _qk_norm(d, dtype, dev, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale), strides)
+        check(load().gdn_qk_norm_rope_fwd(ctypes.byref(a), _raw_stream(dev)), "gdn_qk_norm_rope_fwd")
     return q_out, k_out
 
 
@@ -737,46 +739,42 @@ def gdn_qk_norm_rope_bwd(q, k, positions=None, inv_freq=None, *, grad_q, grad_k=
     """Reverse mode of gdn_qk_norm_rope_fwd for the gradients ``grad_q``, ``grad_k`` of its results.
     Returns dq, dk in the inputs' dtype and dq_norm_w, dk_norm_w [d] fp32 (those that apply)."""
     with _on(q, stream):
-        _same_device(q, k=k, positions=positions, inv_freq=inv_freq, q_norm_w=q_norm_w, k_norm_w=k_norm_w,
-                     grad_q=grad_q, grad_k=grad_k, workspace=workspace)
-        _shape("grad_q", grad_q, q.shape)
-        _same_dtype(q, grad_q=grad_q, grad_k=grad_k)
-        out = {"dq": torch.empty(q.shape, dtype=q.dtype, device=q.device)}
+        dev, dtype, T, Hq, Hk, d, pq, pk, strides = _qk_inputs(q, k)
+        out = {"dq": q.new_empty(q.shape)}
         if k is not None:
-            if grad_k is None:
-                raise GdnError("grad_k is required with k")
-            _shape("grad_k", grad_k, k.shape)
-            out["dk"] = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            out["dk"] = k.new_empty(k.shape)
         for name, w in (("dq_norm_w", q_norm_w), ("dk_norm_w", k_norm_w)):
             if w is not None:
-                out[name] = torch.empty(w.shape, dtype=torch.float32, device=q.device)
-        norm = _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
-        a = _qk_args(QkBwdArgs, q, k, positions, norm, grad_q_out=_ptr(grad_q), grad_k_out=_ptr(grad_k),
-                     grad_q=_ptr(out["dq"]), grad_k=_ptr(out.get("dk")), grad_q_norm_w=_ptr(out.get("dq_norm_w")),
-                     grad_k_norm_w=_ptr(out.get("dk_norm_w")))
+                out[name] = q.new_empty((d,), dtype=torch.float32)
+        ptr = {name: t.data_ptr() for name, t in out.items()}
+        a = QkBwdArgs(pq, pk, _dense("positions", positions, (T,), torch.int32, dev),
+                      _dense("grad_q", grad_q, q.shape, dtype, dev),
+                      _dense("grad_k", grad_k, None if k is None else k.shape, dtype, dev), ptr["dq"], ptr.get("dk"),
+                      ptr.get("dq_norm_w"), ptr.get("dk_norm_w"), T, Hq, Hk, d, _dt(q),
+                      _qk_norm(d, dtype, dev, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale), strides)
         lib = load()
         need = lib.gdn_qk_norm_rope_bwd_workspace_size(ctypes.byref(a))
-        ws = _workspace(need, q.device, workspace)
-        check(lib.gdn_qk_norm_rope_bwd(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_qk_norm_rope_bwd")
+        ws, keep = _bytes(need, q, workspace)
+        check(lib.gdn_qk_norm_rope_bwd(ctypes.byref(a), ws, need, _raw_stream(dev)), "gdn_qk_norm_rope_bwd")
     return out
-
-
-def _attn_args(cls, q, k, v, cu, scale, window, **more):
-    _packed("q", q)
-    T, Hq, d = q.shape
-    _packed("k", k, T, d)
-    _shape("v", v, k.shape)
-    _same_dtype(q, k=k, v=v)
-    (pq, sq), (pk, sk), (pv, sv) = _tok(q, 1), _tok(k, 1), _tok(v, 1)
-    return cls(q=pq, k=pk, v=pv, cu_seqlens=_ptr(cu), T=T, nseq=cu.numel() - 1, Hq=Hq, Hk=k.shape[1], d=d,
-               window=window, scale=d ** -0.5 if scale is None else scale, dtype=_dt(q),
-               strides=Strides(q=sq, k=sk, v=sv), **more)
 
 
 def gdn_attn_fwd_cache_size(q, k, v, cu_seqlens) -> int:
     """Bytes of the cache gdn_attn_fwd(..., bwd_cache=) fills for gdn_attn_bwd."""
-    cu = _cu_seqlens(cu_seqlens, q.device, q.shape[0])
-    return int(load().gdn_attn_fwd_cache_size(ctypes.byref(_attn_args(AttnFwdArgs, q, k, v, cu, None, 0))))
+    T, Hq, d = q.shape
+    nseq = (cu_seqlens.numel() if torch.is_tensor(cu_seqlens) else len(cu_seqlens)) - 1
+    a = AttnFwdArgs(T=T, nseq=nseq, Hq=Hq, Hk=k.shape[1], d=d)
+    return int(load().gdn_attn_fwd_cache_size(ctypes.byref(a)))
+
+
+def _qkv(q, k, v):
+    """(device, dtype, T, Hq, Hk, d, addresses of q, k, v, Strides) of packed q, k, v."""
+    dev, dtype = q.get_device(), q.dtype
+    pq, sq = _packed("q", q, (-1, -1, -1), dtype, dev)
+    T, Hq, d = q.shape
+    pk, sk = _packed("k", k, (T, -1, d), dtype, dev)
+    pv, sv = _packed("v", v, k.shape, dtype, dev)
+    return dev, dtype, T, Hq, k.shape[1], d, pq, pk, pv, Strides(sq, sk, sv)
 
 
 def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: int = 0, o=None,
@@ -786,18 +784,18 @@ def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: 
     unless given; ``window``: 0, or how many tokens, itself included, a token sees.  Returns o; rows
     outside every sequence stay as they were (unset in an ``o`` made here)."""
     with _on(q, stream):
-        _same_device(q, k=k, v=v, o=o, bwd_cache=bwd_cache, workspace=workspace)
-        cu = _cu_seqlens(cu_seqlens, q.device, q.shape[0])
+        dev, dtype, T, Hq, Hk, d, pq, pk, pv, strides = _qkv(q, k, v)
+        pcu, nseq, cu = _cu_seqlens(cu_seqlens, dev, T)
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _shape("o", o, q.shape)
-        _same_dtype(q, o=o)
-        a = _attn_args(AttnFwdArgs, q, k, v, cu, scale, window, o=_ptr(o), bwd_cache=_ptr(bwd_cache),
-                       bwd_cache_bytes=0 if bwd_cache is None else bwd_cache.numel() * bwd_cache.element_size())
+            o = q.new_empty(q.shape)
+        a = AttnFwdArgs(pq, pk, pv, pcu, _dense("o", o, q.shape, dtype, dev), T, nseq, Hq, Hk, d, window,
+                        d ** -0.5 if scale is None else scale, _dt(q),
+                        _dense("bwd_cache", bwd_cache, None, torch.uint8, dev),
+                        0 if bwd_cache is None else bwd_cache.numel(), strides)
         lib = load()
         need = lib.gdn_attn_fwd_workspace_size(ctypes.byref(a))
-        ws = _workspace(need, q.device, workspace)
-        check(lib.gdn_attn_fwd(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_attn_fwd")
+        ws, keep = _bytes(need, q, workspace)
+        check(lib.gdn_attn_fwd(ctypes.byref(a), ws, need, _raw_stream(dev)), "gdn_attn_fwd")
     return o
 
 
@@ -807,37 +805,34 @@ def gdn_attn_bwd(q, k, v, cu_seqlens, o, *, grad_o, fwd_cache: torch.Tensor, sca
     """Reverse mode of gdn_attn_fwd from its output ``o`` and the cache it filled.  Returns dq, dk, dv
     in bf16 (``dq``, ``dk``, ``dv``: buffers to fill; rows outside every sequence stay as they were)."""
     with _on(q, stream):
-        _same_device(q, k=k, v=v, o=o, grad_o=grad_o, fwd_cache=fwd_cache, dq=dq, dk=dk, dv=dv, workspace=workspace)
-        cu = _cu_seqlens(cu_seqlens, q.device, q.shape[0])
-        like = lambda t, given: torch.empty(t.shape, dtype=t.dtype, device=t.device) if given is None else given
-        out = {"dq": like(q, dq), "dk": like(k, dk), "dv": like(v, dv)}
-        for name, t, ref in (("o", o, q), ("grad_o", grad_o, q), ("dq", out["dq"], q), ("dk", out["dk"], k),
-                             ("dv", out["dv"], k)):
-            _shape(name, t, ref.shape)
-            _same_dtype(q, **{name: t})
-        a = _attn_args(AttnBwdArgs, q, k, v, cu, scale, window, o=_ptr(o), grad_o=_ptr(grad_o),
-                       grad_q=_ptr(out["dq"]), grad_k=_ptr(out["dk"]), grad_v=_ptr(out["dv"]),
-                       fwd_cache=_ptr(fwd_cache), fwd_cache_bytes=fwd_cache.numel() * fwd_cache.element_size())
+        dev, dtype, T, Hq, Hk, d, pq, pk, pv, strides = _qkv(q, k, v)
+        pcu, nseq, cu = _cu_seqlens(cu_seqlens, dev, T)
+        dq = q.new_empty(q.shape) if dq is None else dq
+        dk = k.new_empty(k.shape) if dk is None else dk
+        dv = k.new_empty(k.shape) if dv is None else dv
+        a = AttnBwdArgs(pq, pk, pv, pcu, _dense("o", o, q.shape, dtype, dev), _dense("grad_o", grad_o, q.shape, dtype, dev),
+                        _dense("dq", dq, q.shape, dtype, dev), _dense("dk", dk, k.shape, dtype, dev),
+                        _dense("dv", dv, k.shape, dtype, dev), T, nseq, Hq, Hk, d, window,
+                        d ** -0.5 if scale is None else scale, _dt(q),
+                        _dense("fwd_cache", fwd_cache, None, torch.uint8, dev), fwd_cache.numel(), strides)
         lib = load()
         need = lib.gdn_attn_bwd_workspace_size(ctypes.byref(a))
-        ws = _workspace(need, q.device, workspace)
-        check(lib.gdn_attn_bwd(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_attn_bwd")
-    return out
+        ws, keep = _bytes(need, q, workspace)
+        check(lib.gdn_attn_bwd(ctypes.byref(a), ws, need, _raw_stream(dev)), "gdn_attn_bwd")
+    return {"dq": dq, "dk": dk, "dv": dv}
 
 
-def _cache_dims(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, dtype):
-    """(num_pages, page_size, max_pages) of a paged cache [num_pages, page_size, Hk, d]."""
-    if k_cache.dim() != 4 or tuple(k_cache.shape[2:]) != (Hk, d):
+def _cache_args(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, dtype, dev):
+    """Addresses of (k_cache, v_cache, block_table, context_lens), and (num_pages, page_size, max_pages),
+    of a paged cache [num_pages, page_size, Hk, d]."""
+    if k_cache.dim() != 4 or k_cache.shape[2:] != (Hk, d):
         raise GdnError(f"k_cache has shape {tuple(k_cache.shape)}: expected [num_pages, page_size, {Hk}, {d}]")
-    _shape("v_cache", v_cache, k_cache.shape)
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
-        raise GdnError(f"the caches have dtypes {k_cache.dtype}, {v_cache.dtype}, expected {dtype}")
-    _i32("block_table", block_table)
-    _i32("context_lens", context_lens)
     if block_table.dim() != 2 or block_table.shape[0] != nseq:
         raise GdnError(f"block_table has shape {tuple(block_table.shape)}: expected [{nseq}, max_pages]")
-    _shape("context_lens", context_lens, (nseq,))
-    return k_cache.shape[0], k_cache.shape[1], block_table.shape[1]
+    return ((_dense("k_cache", k_cache, None, dtype, dev), _dense("v_cache", v_cache, k_cache.shape, dtype, dev),
+             _dense("block_table", block_table, None, torch.int32, dev),
+             _dense("context_lens", context_lens, (nseq,), torch.int32, dev)),
+            (k_cache.shape[0], k_cache.shape[1], block_table.shape[1]))
 
 
 def gdn_kv_append(k, v, k_cache, v_cache, block_table, context_lens, *, cu_seqlens=None, q=None, inv_freq=None,
@@ -849,33 +844,27 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, context_lens, *, cu_seqle
     [T,Hq,d], the same norm and rotation of q.  Returns (q_out or None, k_out or None: the keys as
     cached, with ``want_k``)."""
     with _on(k, stream):
-        _same_device(k, v=v, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens, q=q,
-                     inv_freq=inv_freq, q_norm_w=q_norm_w, k_norm_w=k_norm_w, q_out=q_out, k_out=k_out)
-        _packed("k", k)
+        dev, dtype = k.get_device(), k.dtype
+        pk, sk = _packed("k", k, (-1, -1, -1), dtype, dev)
         T, Hk, d = k.shape
-        _shape("v", v, k.shape)
-        _same_dtype(k, v=v, q=q, q_out=q_out, k_out=k_out)
-        cu = _cu_seqlens(cu_seqlens, k.device, T)
-        nseq = T if cu is None else cu.numel() - 1
-        pages, page, most = _cache_dims(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, k.dtype)
+        pv, sv = _packed("v", v, k.shape, dtype, dev)
+        pcu, nseq, cu = (None, T, None) if cu_seqlens is None else _cu_seqlens(cu_seqlens, dev, T)
+        (pkc, pvc, ptab, pctx), pages = _cache_args(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, dtype, dev)
+        pq, sq, Hq = None, 0, 0
         if q is not None:
-            _packed("q", q, T, d)
+            pq, sq = _packed("q", q, (T, -1, d), dtype, dev)
+            Hq = q.shape[1]
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            _shape("q_out", q_out, q.shape)
+                q_out = q.new_empty(q.shape)
         elif q_out is not None:
             raise GdnError("q_out needs q")
         if want_k and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-        _shape("k_out", k_out, k.shape)
-        norm = _qk_norm(q, k, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
-        (pq, sq), (pk, sk), (pv, sv) = _tok(q, 1), _tok(k, 1), _tok(v, 1)
-        a = KvAppendArgs(q=pq, k=pk, v=pv, cu_seqlens=_ptr(cu), context_lens=_ptr(context_lens),
-                         block_table=_ptr(block_table), q_out=_ptr(q_out), k_out=_ptr(k_out), k_cache=_ptr(k_cache),
-                         v_cache=_ptr(v_cache), T=T, nseq=nseq, Hq=0 if q is None else q.shape[1], Hk=Hk, d=d,
-                         num_pages=pages, page_size=page, max_pages=most, dtype=_dt(k), norm=norm,
-                         strides=Strides(q=sq, k=sk, v=sv))
-        check(load().gdn_kv_append(ctypes.byref(a), _stream(None)), "gdn_kv_append")
+            k_out = k.new_empty(k.shape)
+        a = KvAppendArgs(pq, pk, pv, pcu, pctx, ptab, _dense("q_out", q_out, None if q is None else q.shape, dtype, dev),
+                         _dense("k_out", k_out, k.shape, dtype, dev), pkc, pvc, T, nseq, Hq, Hk, d, *pages, _dt(k),
+                         _qk_norm(d, dtype, dev, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale),
+                         Strides(sq, sk, sv))
+        check(load().gdn_kv_append(ctypes.byref(a), _raw_stream(dev)), "gdn_kv_append")
     return q_out, k_out
 
 
@@ -885,23 +874,17 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, context_lens, *, scale: Op
     tokens each, this one's included.  ``max_context``: a bound on the lengths that the caller knows
     (0: the block table's reach).  Returns o [N,Hq,d]."""
     with _on(q, stream):
-        _same_device(q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, context_lens=context_lens, o=o,
-                     workspace=workspace)
-        _packed("q", q)
+        dev, dtype = q.get_device(), q.dtype
+        pq, sq = _packed("q", q, (-1, -1, -1), dtype, dev)
         N, Hq, d = q.shape
         Hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
-        pages, page, most = _cache_dims(k_cache, v_cache, block_table, context_lens, N, Hk, d, q.dtype)
+        (pkc, pvc, ptab, pctx), pages = _cache_args(k_cache, v_cache, block_table, context_lens, N, Hk, d, dtype, dev)
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _shape("o", o, q.shape)
-        _same_dtype(q, o=o)
-        pq, sq = _tok(q, 1)
-        a = AttnDecodeArgs(q=pq, k_cache=_ptr(k_cache), v_cache=_ptr(v_cache), block_table=_ptr(block_table),
-                           context_lens=_ptr(context_lens), o=_ptr(o), N=N, Hq=Hq, Hk=Hk, d=d, num_pages=pages,
-                           page_size=page, max_pages=most, max_context=max_context, window=window,
-                           scale=d ** -0.5 if scale is None else scale, dtype=_dt(q), strides=Strides(q=sq))
+            o = q.new_empty(q.shape)
+        a = AttnDecodeArgs(pq, pkc, pvc, ptab, pctx, _dense("o", o, q.shape, dtype, dev), N, Hq, Hk, d, *pages,
+                           max_context, window, d ** -0.5 if scale is None else scale, _dt(q), Strides(sq))
         lib = load()
         need = lib.gdn_attn_decode_workspace_size(ctypes.byref(a))
-        ws = _workspace(need, q.device, workspace)
-        check(lib.gdn_attn_decode(ctypes.byref(a), _ptr(ws), need, _stream(None)), "gdn_attn_decode")
+        ws, keep = _bytes(need, q, workspace)
+        check(lib.gdn_attn_decode(ctypes.byref(a), ws, need, _raw_stream(dev)), "gdn_attn_decode")
     return o
