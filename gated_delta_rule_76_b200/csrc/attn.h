@@ -37,11 +37,11 @@ struct QkParams {
     int T, Hq, Hk;
     RopeParams rope;
     AppendParams app;
-    float* partials;           // backward: [CTAs][2][d]
+    float* partials;           // backward: [CTAs][d]
 };
 
 cudaError_t qk_norm_rope_fwd(const QkParams& p, int d, bool bf16, cudaStream_t st);
-size_t qk_norm_rope_bwd_partials(int T, int d);  // floats
+size_t qk_norm_rope_bwd_partials(int T, int Hq, int Hk, int d);  // floats
 // dq_w, dk_w [d] (NULL without the norm)
 cudaError_t qk_norm_rope_bwd(const QkParams& p, int d, bool bf16, void* dq, void* dk, float* dq_w, float* dk_w,
                              cudaStream_t st);

@@ -189,9 +189,9 @@ gdn_status gdn_qk_norm_rope_fwd(const gdn_qk_fwd_args* a, gdn_stream stream) {
 }
 
 size_t gdn_qk_norm_rope_bwd_workspace_size(const gdn_qk_bwd_args* a) {
-    if (!a || a->T < 0 || a->T >= kMaxTokens || a->d < 1 || a->d > 128) return 0;
+    if (!a || a->T < 0 || a->T >= kMaxTokens || a->Hq < 1 || a->Hk < 0 || a->d < 1 || a->d > 128) return 0;
     if (!a->norm.q_norm_w && !a->norm.k_norm_w) return 0;
-    return 256 + align256(qk_norm_rope_bwd_partials((int)a->T, (int)a->d) * sizeof(float));
+    return 256 + align256(qk_norm_rope_bwd_partials((int)a->T, (int)a->Hq, (int)a->Hk, (int)a->d) * sizeof(float));
 }
 
 gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_bwd_args* a, void* workspace, size_t workspace_bytes, gdn_stream stream) {

@@ -2,21 +2,22 @@
 // cache's append, which does the same on the way into the cache (the formulas stand at gdn_qk_norm
 // in gdn.h).
 //
-// A head row of d channels is held by d / 8 lanes, 8 channels (one 16-byte bf16 vector) each, so a warp
-// holds 2 rows of 128 or 4 of 64.  A warp takes one token and walks (a part of) its heads, so that all
-// that depends on the token and the channel alone is formed once, in registers:
-//     y_i = r (x_i A_i + x_p(i) B_i),   A_i = w_i cos, B_i = -+ w_p(i) sin,   r = 1 / sqrt(mean x^2 + eps)
-// with p(i) the partner of channel i in its pair.  In the half layout the partner is i +- rot / 2, the same
-// register of another lane (rot / 2 is a multiple of 8), and the raw words are exchanged, before
-// the row's reduction ends; in the interleaved layout it is the neighbouring register.
+// A lane holds 16 channels of a head row, two 16-byte vectors (of bf16), chosen so that both channels of each
+// of its 8 pairs are its own: in the half layout vectors v and v + rot / 16 (rot / 2 is a multiple of
+// 8 channels), in the interleaved layout neighbouring ones; vectors that are not rotated pair up among themselves.
+// a and b are the first and second channels of the pairs, and only loading and storing know the layout.
+// Eight lanes hold a row of 128, four a row of 64: a warp 4 or 8 rows.
 //
+// A warp takes one token and walks (a part of) its heads of one kind (q, k or v), so that all that depends on the
+// token and the channel alone is formed once, in registers:
+//     y_a = r (a (w_a cos) - b (w_b sin)),  y_b = r (b (w_b cos) + a (w_a sin)),  r = 1 / sqrt(mean x^2 + eps).
 // Angles: p * f in turns is a product in 64 bits, of which only the fraction is kept, so that positions
 // of millions lose nothing; fp32 sincospi then sees an argument in [-1, 1].  A warp forms its token's
-// rot / 2 angles once, two a lane.
+// rot / 2 angles once, two a lane at most.
 //
 // Bound: HBM, each row read once and written once (backward: two rows read, one written).  What it
-// takes is enough loads in flight and few instructions a channel: the rows of a batch of kBatch are all
-// loaded before the first is used.
+// takes is enough loads in flight (the rows of a batch are all loaded before the first is used) and few
+// instructions a channel (no exchange between lanes but the row's sum; packed fp32 pairs).
 #include <cuda_bf16.h>
 
 #include "attn.h"
@@ -30,7 +31,28 @@ constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kHalfMax = 64;  // rot / 2 at most
 
-// Eight channels as they lie in memory.
+// ---- pairs of fp32 in one 64-bit register ------------------------------------------------------
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_get(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// ---- eight channels as they lie in memory ----------------------------------------------------
 template <class T> struct Raw;
 template <> struct Raw<__nv_bfloat16> { uint32_t w[4]; };
 template <> struct Raw<float> { uint32_t w[8]; };
@@ -55,6 +77,12 @@ __device__ __forceinline__ Raw<T> load_raw(const T* p, bool vec) {
     }
     return r;
 }
+template <class T>
+__device__ __forceinline__ void store_raw(T* p, const Raw<T>& r) {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Raw<T>) / 4); i += 4)
+        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
+}
 __device__ __forceinline__ void unpack(const Raw<__nv_bfloat16>& r, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -66,61 +94,99 @@ __device__ __forceinline__ void unpack(const Raw<float>& r, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(r.w[i]);
 }
-template <class T>
-__device__ __forceinline__ void store_raw(T* p, const Raw<T>& r) {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(Raw<T>) / 4); i += 4)
-        reinterpret_cast<uint4*>(p)[i / 4] = make_uint4(r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]);
-}
-__device__ __forceinline__ Raw<float> pack(const float (&x)[8], float) {
-    Raw<float> r;
+__device__ __forceinline__ void pack(const float (&x)[8], Raw<float>& r) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(x[i]);
-    return r;
 }
-__device__ __forceinline__ Raw<__nv_bfloat16> pack(const float (&x)[8], __nv_bfloat16) {
-    Raw<__nv_bfloat16> r;
+__device__ __forceinline__ void pack(const float (&x)[8], Raw<__nv_bfloat16>& r) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
         r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
     }
+}
+
+// ---- a lane's 16 channels ---------------------------------------------------------------------
+// Where they stand: the first channels of its two vectors, and the first of its 8 angles (-1: not rotated).
+struct Place {
+    int c0, c1, angle;
+};
+template <int D, bool IL>
+__device__ __forceinline__ Place place_of(int rot) {
+    const int l = (threadIdx.x & 31) % (D / 16);
+    if (IL) return Place{16 * l, 16 * l + 8, 16 * l < rot ? 8 * l : -1};
+    const int hv = rot >> 4;  // vectors of a half
+    if (l < hv) return Place{8 * l, 8 * (l + hv), 8 * l};
+    return Place{8 * (2 * hv + 2 * (l - hv)), 8 * (2 * hv + 2 * (l - hv)) + 8, -1};
+}
+
+template <class T> struct Raw2 { Raw<T> v0, v1; };
+template <class T>
+__device__ __forceinline__ Raw2<T> load_row(const T* p, const Place& pl, bool vec) {
+    return Raw2<T>{load_raw(p + pl.c0, vec), load_raw(p + pl.c1, vec)};
+}
+template <class T>
+__device__ __forceinline__ void store_row(T* p, const Place& pl, const Raw2<T>& r) {
+    store_raw(p + pl.c0, r.v0);
+    store_raw(p + pl.c1, r.v1);
+}
+// The 8 pairs as 4 + 4 packed registers, and back.
+template <bool IL, class T>
+__device__ __forceinline__ void split(const Raw2<T>& r, f2 (&a)[4], f2 (&b)[4]) {
+    float x[8], y[8];
+    unpack(r.v0, x);
+    unpack(r.v1, y);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (IL) {
+            const int e = 4 * (i & 1);
+            a[i] = i < 2 ? f2_of(x[e], x[e + 2]) : f2_of(y[e], y[e + 2]);
+            b[i] = i < 2 ? f2_of(x[e + 1], x[e + 3]) : f2_of(y[e + 1], y[e + 3]);
+        } else {
+            a[i] = f2_of(x[2 * i], x[2 * i + 1]);
+            b[i] = f2_of(y[2 * i], y[2 * i + 1]);
+        }
+    }
+}
+template <bool IL, class T>
+__device__ __forceinline__ Raw2<T> join(const f2 (&a)[4], const f2 (&b)[4]) {
+    float x[8], y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a0, a1, b0, b1;
+        f2_get(a[i], a0, a1);
+        f2_get(b[i], b0, b1);
+        if (IL) {
+            const int e = 4 * (i & 1);
+            float(&o)[8] = i < 2 ? x : y;
+            o[e] = a0; o[e + 1] = b0; o[e + 2] = a1; o[e + 3] = b1;
+        } else {
+            x[2 * i] = a0; x[2 * i + 1] = a1;
+            y[2 * i] = b0; y[2 * i + 1] = b1;
+        }
+    }
+    Raw2<T> r;
+    pack(x, r.v0);
+    pack(y, r.v1);
     return r;
 }
 
-// Sum over the d / 8 lanes of a row.
+// Sum over the d / 16 lanes of a row.
 template <int D>
 __device__ __forceinline__ float row_sum(float x) {
 #pragma unroll
-    for (int o = D / 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = D / 32; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
     return x;
 }
-
-// Where this lane's eight channels stand in the rotation.
-struct Place {
-    int c0;        // first channel
-    bool in;       // among the rotated ones
-    bool lower;    // half layout: first of its pairs
-    int src;       // half layout: the lane that holds the partners
-    int pc0;       // half layout: the partners' first channel
-};
-template <int D>
-__device__ __forceinline__ Place place_of(const RopeParams& r) {
-    Place pl;
-    const int lane = threadIdx.x & 31, half = r.rot >> 1;
-    pl.c0 = (lane % (D / 8)) * 8;
-    pl.in = pl.c0 < r.rot;
-    pl.lower = pl.c0 < half;
-    const bool swap = pl.in && !r.interleaved;
-    pl.src = swap ? (pl.lower ? lane + (half >> 3) : lane - (half >> 3)) : lane;
-    pl.pc0 = swap ? (pl.lower ? pl.c0 + half : pl.c0 - half) : pl.c0;
-    return pl;
+__device__ __forceinline__ float f2_sum(f2 v) {
+    float a, b;
+    f2_get(v, a, b);
+    return a + b;
 }
 
-// cos and signed sin of this lane's channels at position pos (1 and 0 where nothing is rotated):
-//     y_i = x_i c_i + x_p(i) s_i.  Warp-collective; tb: the warp's [2][kHalfMax] floats.
-__device__ __forceinline__ void angles(const RopeParams& r, const Place& pl, int pos, float* tb, float (&c)[8],
-                                       float (&s)[8]) {
+// cos and sin of this lane's pairs at position pos (1 and 0 where nothing is rotated).
+// Warp-collective; tb: the warp's [2][kHalfMax] floats.
+__device__ __forceinline__ void angles(const RopeParams& r, const Place& pl, int pos, float* tb, f2 (&c)[4], f2 (&s)[4]) {
     const int half = r.rot >> 1;
     __syncwarp();
     for (int j = threadIdx.x & 31; j < half; j += 32) {
@@ -132,57 +198,25 @@ __device__ __forceinline__ void angles(const RopeParams& r, const Place& pl, int
     }
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        c[i] = 1.f;
-        s[i] = 0.f;
-    }
-    if (!pl.in) return;
-    if (r.interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = tb[(pl.c0 + i) >> 1];
-            s[i] = (i & 1) ? tb[kHalfMax + ((pl.c0 + i) >> 1)] : -tb[kHalfMax + ((pl.c0 + i) >> 1)];
-        }
-    } else {
-        const int j = pl.lower ? pl.c0 : pl.pc0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            c[i] = tb[j + i];
-            s[i] = pl.lower ? -tb[kHalfMax + j + i] : tb[kHalfMax + j + i];
+    for (int i = 0; i < 4; ++i) {
+        c[i] = f2_of(1.f, 1.f);
+        s[i] = f2_of(0.f, 0.f);
+        if (pl.angle >= 0) {
+            const float2 x = *reinterpret_cast<const float2*>(tb + pl.angle + 2 * i);
+            const float2 y = *reinterpret_cast<const float2*>(tb + kHalfMax + pl.angle + 2 * i);
+            c[i] = f2_of(x.x, x.y);
+            s[i] = f2_of(y.x, y.y);
         }
     }
 }
 
-// The partners of x (whose words are r).  Every lane of the warp calls it.
-template <class T>
-__device__ __forceinline__ void partners(const Raw<T>& r, const float (&x)[8], const Place& pl, bool interleaved,
-                                         float (&y)[8]) {
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = x[i ^ 1];
+template <bool IL, class T>
+__device__ __forceinline__ void weights(const void* w, const Place& pl, f2 (&wa)[4], f2 (&wb)[4]) {
+    if (w) {
+        split<IL>(load_row(static_cast<const T*>(w), pl, true), wa, wb);
     } else {
-        Raw<T> o;
 #pragma unroll
-        for (int i = 0; i < (int)(sizeof(Raw<T>) / 4); ++i) o.w[i] = __shfl_sync(0xffffffffu, r.w[i], pl.src);
-        unpack(o, y);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = pl.in ? y[i] : 0.f;  // not x: 0 times an infinity is not 0
-}
-
-// The norm weights of this lane's channels and of their partners (1 without a norm).
-template <class T>
-__device__ __forceinline__ void weights(const void* w, const Place& pl, bool interleaved, float (&own)[8],
-                                        float (&partner)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) own[i] = partner[i] = 1.f;
-    if (!w) return;
-    unpack(load_raw(static_cast<const T*>(w) + pl.c0, true), own);
-    if (interleaved) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) partner[i] = own[i ^ 1];
-    } else {
-        unpack(load_raw(static_cast<const T*>(w) + pl.pc0, true), partner);
+        for (int i = 0; i < 4; ++i) wa[i] = wb[i] = f2_of(1.f, 1.f);
     }
 }
 
@@ -218,243 +252,288 @@ __device__ __forceinline__ void find_token(const AppendParams& a, int t, int& po
     slot = (int64_t)page * a.page_size + (p - page_no * a.page_size);
 }
 
-// Rows of one kind (q, k or v) that a warp takes of its token: heads part * RPW + (lane's row), step
-// parts * RPW.  batch(n, ...) sees kBatch of them at a time, loaded together.
-constexpr int kBatch = 4;
+constexpr int kBatch = 4;  // rows a lane loads before it uses the first
 
-// One kind's rows, normalised and rotated, to dst (and dst2), rows of D elements from there on.
-template <class T, int D>
-__device__ __forceinline__ void rope_rows(const T* src, bool vec, int H, T* dst, T* dst2, bool norm, float eps,
-                                          bool interleaved, const Place& pl, const float (&A)[8], const float (&B)[8],
-                                          int part, int parts) {
-    constexpr int RPW = 256 / D;
-    const int r0 = (threadIdx.x & 31) / (D / 8), step = parts * RPW;
-    for (int base = part * RPW; base < H; base += kBatch * step) {
-        Raw<T> raw[kBatch];
+// A warp's rows of one kind, from src to dst and dst2 (either may be NULL), heads head0, head0 + step, ...;
+// ROPE: normalised (with w) and rotated by c, s, else copied.  `before` runs while the first rows are on
+// their way: it forms c and s.
+template <class T, int D, bool IL, bool ROPE, class F>
+__device__ __forceinline__ void fwd_rows(const T* src, bool vec, int H, T* dst, T* dst2, const void* w, float eps,
+                                         const Place& pl, f2 (&c)[4], f2 (&s)[4], int base, int step, F before) {
+    const int r0 = (threadIdx.x & 31) / (D / 16);
+    f2 ca[4], sb[4], cb[4], sa[4];  // w_a cos, -w_b sin, w_b cos, w_a sin
+    bool ready = false;
+    for (; base < H; base += kBatch * step) {
+        Raw2<T> raw[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = base + u * step + r0;
-            if (h < H) raw[u] = load_raw(src + (int64_t)h * D + pl.c0, vec);
-            else raw[u] = Raw<T>{};
+            raw[u] = Raw2<T>{};
+            if (h < H) raw[u] = load_row(src + (int64_t)h * D, pl, vec);
+        }
+        if (ROPE && !ready) {
+            f2 wa[4], wb[4];
+            weights<IL, T>(w, pl, wa, wb);
+            before();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                ca[i] = f2_mul(wa[i], c[i]);
+                cb[i] = f2_mul(wb[i], c[i]);
+                sa[i] = f2_mul(wa[i], s[i]);
+                sb[i] = f2_mul(f2_mul(wb[i], s[i]), f2_of(-1.f, -1.f));
+            }
+            ready = true;
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int h = base + u * step + r0;
             if (base + u * step >= H) break;  // the whole warp
-            float x[8], y[8];
-            unpack(raw[u], x);
-            partners(raw[u], x, pl, interleaved, y);
-            float r = 1.f;
-            if (norm) {
-                float ss = 0.f;
+            Raw2<T> out = raw[u];
+            if (ROPE) {
+                f2 a[4], b[4];
+                split<IL>(raw[u], a, b);
+                f2 r = f2_of(1.f, 1.f);
+                if (w) {
+                    f2 ss = f2_mul(a[0], a[0]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-                r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+                    for (int i = 1; i < 4; ++i) ss = f2_fma(a[i], a[i], ss);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ss = f2_fma(b[i], b[i], ss);
+                    const float x = rsqrtf(row_sum<D>(f2_sum(ss)) * (1.f / D) + eps);
+                    r = f2_of(x, x);
+                }
+                if (pl.angle >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const f2 ya = f2_fma(a[i], ca[i], f2_mul(b[i], sb[i]));
+                        const f2 yb = f2_fma(b[i], cb[i], f2_mul(a[i], sa[i]));
+                        a[i] = f2_mul(r, ya);
+                        b[i] = f2_mul(r, yb);
+                    }
+                } else {  // not 0 times the partner, which may be infinite
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        a[i] = f2_mul(r, f2_mul(a[i], ca[i]));
+                        b[i] = f2_mul(r, f2_mul(b[i], cb[i]));
+                    }
+                }
+                out = join<IL, T>(a, b);
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = r * fmaf(x[i], A[i], y[i] * B[i]);
             if (h < H) {
-                const Raw<T> out = pack(y, T{});
-                if (dst) store_raw(dst + (int64_t)h * D + pl.c0, out);
-                if (dst2) store_raw(dst2 + (int64_t)h * D + pl.c0, out);
+                if (dst) store_row(dst + (int64_t)h * D, pl, out);
+                if (dst2) store_row(dst2 + (int64_t)h * D, pl, out);
             }
         }
     }
 }
 
-template <class T, int D, bool APPEND>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const QkParams p, int parts) {
-    constexpr int RPW = 256 / D;
-    __shared__ float tb[kWarps][2 * kHalfMax];
-    const int warp = threadIdx.x >> 5;
-    const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
-    const int64_t t = unit / parts;
-    const int part = (int)(unit - t * parts);
-    if (t >= p.T) return;
+// 2^parts_log warps share a token's heads.
+template <class T, int D, bool IL, bool APPEND>
+__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const QkParams p, int parts_log) {
+    constexpr int RPW = 512 / D;
+    __shared__ __align__(16) float tb[kWarps][2 * kHalfMax];
+    const int64_t unit = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+    const int t = (int)(unit >> parts_log);
+    if (unit >> parts_log >= p.T) return;
+    const int base = ((int)unit & ((1 << parts_log) - 1)) * RPW, step = RPW << parts_log;
     int pos = 0;
-    int64_t slot = 0;
+    int64_t slot = kNoSlot;
     if (APPEND) {
-        find_token(p.app, (int)t, pos, slot);
+        find_token(p.app, t, pos, slot);
         if (slot == kOutside) return;
     } else if (p.positions) {
         pos = __ldg(p.positions + t);
     }
-    const Place pl = place_of<D>(p.rope);
-    const bool il = p.rope.interleaved != 0;
-    float c[8], s[8];
-    angles(p.rope, pl, pos, tb[warp], c, s);
-    auto rows = [&](const Rows& src, const void* w, int H, T* dst, T* dst2) {
-        float own[8], partner[8];
-        weights<T>(w, pl, il, own, partner);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            own[i] *= c[i];
-            partner[i] *= s[i];
-        }
-        rope_rows<T, D>(static_cast<const T*>(src.p) + t * src.stride, src.vec != 0, H, dst, dst2, w != nullptr,
-                        p.rope.eps, il, pl, own, partner, part, parts);
+    const Place pl = place_of<D, IL>(p.rope.rot);
+    f2 c[4], s[4];
+    bool have = false;
+    auto turn = [&]() {
+        if (!have) angles(p.rope, pl, pos, tb[threadIdx.x >> 5], c, s);
+        have = true;
     };
-    if (p.Hq) rows(p.q, p.rope.q_w, p.Hq, static_cast<T*>(p.q_out) + t * p.Hq * D, static_cast<T*>(nullptr));
-    T* k_out = p.k_out ? static_cast<T*>(p.k_out) + t * p.Hk * D : nullptr;
-    if constexpr (APPEND) {
-        const int64_t at = slot * p.Hk * D;
-        T* kc = slot >= 0 ? static_cast<T*>(p.app.k_cache) + at : nullptr;
-        if (kc || k_out) rows(p.k, p.rope.k_w, p.Hk, k_out, kc);
-        if (slot >= 0) {
-            const T* v = static_cast<const T*>(p.v.p) + t * p.v.stride;
-            T* vc = static_cast<T*>(p.app.v_cache) + at;
-            for (int h = part * RPW + (threadIdx.x & 31) / (D / 8); h < p.Hk; h += parts * RPW)
-                store_raw(vc + (int64_t)h * D + pl.c0, load_raw(v + (int64_t)h * D + pl.c0, p.v.vec != 0));
-        }
-    } else if (p.Hk) {
-        rows(p.k, p.rope.k_w, p.Hk, k_out, static_cast<T*>(nullptr));
-    }
+    T* none = nullptr;
+    const int64_t q_at = (int64_t)t * p.Hq * D, k_at = (int64_t)t * p.Hk * D;
+    if (p.Hq)
+        fwd_rows<T, D, IL, true>(static_cast<const T*>(p.q.p) + t * p.q.stride, p.q.vec != 0, p.Hq,
+                                 static_cast<T*>(p.q_out) + q_at, none, p.rope.q_w, p.rope.eps, pl, c, s, base, step, turn);
+    T* k_out = p.k_out ? static_cast<T*>(p.k_out) + k_at : none;
+    T* kc = APPEND && slot >= 0 ? static_cast<T*>(p.app.k_cache) + slot * p.Hk * D : none;
+    if (k_out || kc)
+        fwd_rows<T, D, IL, true>(static_cast<const T*>(p.k.p) + t * p.k.stride, p.k.vec != 0, p.Hk, k_out, kc, p.rope.k_w,
+                                 p.rope.eps, pl, c, s, base, step, turn);
+    if (APPEND && slot >= 0)
+        fwd_rows<T, D, IL, false>(static_cast<const T*>(p.v.p) + t * p.v.stride, p.v.vec != 0, p.Hk,
+                                  static_cast<T*>(p.app.v_cache) + slot * p.Hk * D, none, nullptr, 0.f, pl, c, s, base, step,
+                                  turn);
 }
 
 // The reverse mode.  With n = x r w, r = 1 / sqrt(mean x^2 + eps), and gn the gradient of n (the
 // rotation's transpose applied to the gradient of y):
 //     dw = sum over rows of gn x r,     dx = r (gn w - x r^2 mean(gn w x)).
-// The warps walk the tokens in a fixed stride and keep dw in registers, 8 channels of q's and of k's
-// weights a lane; at the end a CTA adds its warps' in shared memory and stores one partial, and
-// rope_dw_kernel adds the CTAs' partials.  Every order is fixed by the sizes.
-template <class T, int D>
-__device__ __forceinline__ void rope_grad_rows(const T* src, bool vec, const T* grad, int H, T* dst, bool norm, float eps,
-                                               bool interleaved, const Place& pl, const float (&w)[8], const float (&c)[8],
-                                               const float (&s)[8], float (&acc)[8]) {
-    constexpr int RPW = 256 / D, BATCH = 2;
-    const int r0 = (threadIdx.x & 31) / (D / 8);
-    for (int base = 0; base < H; base += BATCH * RPW) {
-        Raw<T> rx[BATCH], rg[BATCH];
+// The first `ctas_q` CTAs take q's rows, the others k's, each walking the tokens in a fixed stride; dw stays in
+// registers, 16 channels a lane, until a CTA adds its warps' in shared memory and stores one
+// partial; rope_dw_kernel adds the CTAs'.  Every order is fixed by the sizes.
+template <class T, int D, bool IL>
+__global__ void __launch_bounds__(kThreads, 4) rope_bwd_kernel(const QkParams p, T* __restrict__ dq, T* __restrict__ dk,
+                                                               int ctas_q) {
+    constexpr int RPW = 512 / D, BATCH = 2;
+    __shared__ __align__(16) float tb[kWarps][2 * kHalfMax];
+    __shared__ float red[kWarps * RPW][D];
+    const int warp = threadIdx.x >> 5, r0 = (threadIdx.x & 31) / (D / 16);
+    const bool is_q = (int)blockIdx.x < ctas_q;
+    const int cta = is_q ? blockIdx.x : blockIdx.x - ctas_q, ctas = is_q ? ctas_q : gridDim.x - ctas_q;
+    const int H = is_q ? p.Hq : p.Hk;
+    const Rows& in = is_q ? p.q : p.k;
+    const void* w = is_q ? p.rope.q_w : p.rope.k_w;
+    const bool vec = in.vec != 0;
+    const Place pl = place_of<D, IL>(p.rope.rot);
+    f2 wa[4], wb[4], acca[4], accb[4];
+    weights<IL, T>(w, pl, wa, wb);
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int h = base + u * RPW + r0;
-            rx[u] = rg[u] = Raw<T>{};
-            if (h < H) {
-                rx[u] = load_raw(src + (int64_t)h * D + pl.c0, vec);
-                rg[u] = load_raw(grad + (int64_t)h * D + pl.c0, true);
-            }
-        }
+    for (int i = 0; i < 4; ++i) acca[i] = accb[i] = f2_of(0.f, 0.f);
+    const f2 minus = f2_of(-1.f, -1.f);
+    for (int64_t t = (int64_t)cta * kWarps + warp; t < p.T; t += (int64_t)ctas * kWarps) {
+        const T* src = static_cast<const T*>(in.p) + t * in.stride;
+        const T* grad = static_cast<const T*>(is_q ? p.gq : p.gk) + t * H * D;
+        T* dst = (is_q ? dq : dk) + t * H * D;
+        f2 c[4], s[4];
+        for (int base = 0; base < H; base += BATCH * RPW) {
+            Raw2<T> rx[BATCH], rg[BATCH];
 #pragma unroll
-        for (int u = 0; u < BATCH; ++u) {
-            const int h = base + u * RPW + r0;
-            if (base + u * RPW >= H) break;
-            float g[8], y[8];
-            unpack(rg[u], g);
-            partners(rg[u], g, pl, interleaved, y);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = fmaf(g[i], c[i], -(y[i] * s[i]));  // the transpose turns back
-            if (norm) {
-                float x[8], ss = 0.f, gx = 0.f;
-                unpack(rx[u], x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ss = fmaf(x[i], x[i], ss);
-                    gx = fmaf(g[i] * w[i], x[i], gx);
-                }
-                ss = row_sum<D>(ss);
-                gx = row_sum<D>(gx);
-                // a lane without a row adds nothing, whatever eps is
-                const float r = h < H ? rsqrtf(ss * (1.f / D) + eps) : 0.f, m = r * r * gx * (1.f / D);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[i] = fmaf(g[i] * x[i], r, acc[i]);
-                    g[i] = r * fmaf(g[i], w[i], -(x[i] * m));
+            for (int u = 0; u < BATCH; ++u) {
+                const int h = base + u * RPW + r0;
+                rx[u] = rg[u] = Raw2<T>{};
+                if (h < H) {
+                    rg[u] = load_row(grad + (int64_t)h * D, pl, true);
+                    rx[u] = load_row(src + (int64_t)h * D, pl, vec);
                 }
             }
-            if (h < H) store_raw(dst + (int64_t)h * D + pl.c0, pack(g, T{}));
+            // while the first rows are on their way
+            if (base == 0) angles(p.rope, pl, p.positions ? __ldg(p.positions + t) : 0, tb[warp], c, s);
+#pragma unroll
+            for (int u = 0; u < BATCH; ++u) {
+                const int h = base + u * RPW + r0;
+                if (base + u * RPW >= H) break;
+                f2 ga[4], gb[4];
+                split<IL>(rg[u], ga, gb);
+                if (pl.angle >= 0) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // the transpose turns back
+                        const f2 a = f2_fma(ga[i], c[i], f2_mul(gb[i], s[i]));
+                        gb[i] = f2_fma(gb[i], c[i], f2_mul(f2_mul(ga[i], minus), s[i]));
+                        ga[i] = a;
+                    }
+                }
+                if (w) {
+                    f2 a[4], b[4];
+                    split<IL>(rx[u], a, b);
+                    f2 ss = f2_mul(a[0], a[0]), gx = f2_mul(f2_mul(ga[0], wa[0]), a[0]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (i) {
+                            ss = f2_fma(a[i], a[i], ss);
+                            gx = f2_fma(f2_mul(ga[i], wa[i]), a[i], gx);
+                        }
+                        ss = f2_fma(b[i], b[i], ss);
+                        gx = f2_fma(f2_mul(gb[i], wb[i]), b[i], gx);
+                    }
+                    const float s1 = row_sum<D>(f2_sum(ss)), g1 = row_sum<D>(f2_sum(gx));
+                    // a lane without a row adds nothing, whatever eps is
+                    const float r1 = h < H ? rsqrtf(s1 * (1.f / D) + p.rope.eps) : 0.f;
+                    const float m1 = -r1 * r1 * g1 * (1.f / D);
+                    const f2 r = f2_of(r1, r1), m = f2_of(m1, m1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        acca[i] = f2_fma(f2_mul(ga[i], a[i]), r, acca[i]);
+                        accb[i] = f2_fma(f2_mul(gb[i], b[i]), r, accb[i]);
+                        ga[i] = f2_mul(r, f2_fma(ga[i], wa[i], f2_mul(a[i], m)));
+                        gb[i] = f2_mul(r, f2_fma(gb[i], wb[i], f2_mul(b[i], m)));
+                    }
+                }
+                if (h < H) store_row(dst + (int64_t)h * D, pl, join<IL, T>(ga, gb));
+            }
         }
     }
-}
-
-template <class T, int D>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const QkParams p, T* __restrict__ dq, T* __restrict__ dk) {
-    constexpr int RPW = 256 / D;
-    __shared__ float tb[kWarps][2 * kHalfMax];
-    __shared__ float red[2][kWarps * RPW][D];
-    const int warp = threadIdx.x >> 5;
-    const Place pl = place_of<D>(p.rope);
-    const bool il = p.rope.interleaved != 0;
-    float wq[8], wk[8], aq[8], ak[8], c[8], s[8];
-    {
-        float unused[8];
-        weights<T>(p.rope.q_w, pl, il, wq, unused);
-        weights<T>(p.rope.k_w, pl, il, wk, unused);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) aq[i] = ak[i] = 0.f;
-    for (int64_t t = (int64_t)blockIdx.x * kWarps + warp; t < p.T; t += (int64_t)gridDim.x * kWarps) {
-        angles(p.rope, pl, p.positions ? __ldg(p.positions + t) : 0, tb[warp], c, s);
-        rope_grad_rows<T, D>(static_cast<const T*>(p.q.p) + t * p.q.stride, p.q.vec != 0,
-                             static_cast<const T*>(p.gq) + t * p.Hq * D, p.Hq, dq + t * p.Hq * D, p.rope.q_w != nullptr,
-                             p.rope.eps, il, pl, wq, c, s, aq);
-        if (p.Hk)
-            rope_grad_rows<T, D>(static_cast<const T*>(p.k.p) + t * p.k.stride, p.k.vec != 0,
-                                 static_cast<const T*>(p.gk) + t * p.Hk * D, p.Hk, dk + t * p.Hk * D,
-                                 p.rope.k_w != nullptr, p.rope.eps, il, pl, wk, c, s, ak);
-    }
-    if (!p.partials) return;
-    const int row = threadIdx.x / (D / 8);
+    if (!p.partials || !w) return;
+    const int row = threadIdx.x / (D / 16);
+    const Raw2<float> acc = join<IL, float>(acca, accb);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        red[0][row][pl.c0 + i] = aq[i];
-        red[1][row][pl.c0 + i] = ak[i];
+        red[row][pl.c0 + i] = __uint_as_float(acc.v0.w[i]);
+        red[row][pl.c1 + i] = __uint_as_float(acc.v1.w[i]);
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
-        const int w = e / D, ch = e % D;
+    if (threadIdx.x < D) {
         float sum = 0.f;
 #pragma unroll
-        for (int r = 0; r < kWarps * RPW; ++r) sum += red[w][r][ch];
-        p.partials[(int64_t)blockIdx.x * 2 * D + e] = sum;
+        for (int r = 0; r < kWarps * RPW; ++r) sum += red[r][threadIdx.x];
+        p.partials[(int64_t)blockIdx.x * D + threadIdx.x] = sum;
     }
 }
 
-// dw[c] = sum over the CTAs' partials, 32 channels a CTA, 32 strided slices of the partials each.
-__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partials, int ctas, int d,
+// dw[c] = sum over the CTAs' partials of one kind (blockIdx.y), 32 channels a CTA, 32 strided slices of the
+// partials each.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* __restrict__ partials, int ctas_q, int ctas_k, int d,
                                                        float* __restrict__ dq_w, float* __restrict__ dk_w) {
     __shared__ float red[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;  // channel of [2][d]
+    float* out = blockIdx.y ? dk_w : dq_w;
+    if (!out) return;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    const int first = blockIdx.y ? ctas_q : 0, n = blockIdx.y ? ctas_k : ctas_q;
     float s = 0.f;
-    for (int i = threadIdx.y; i < ctas; i += 32) s += partials[(int64_t)i * 2 * d + c];
+#pragma unroll 8
+    for (int i = threadIdx.y; i < n; i += 32) s += partials[(int64_t)(first + i) * d + c];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y) return;
     s = 0.f;
+#pragma unroll
     for (int i = 0; i < 32; ++i) s += red[i][threadIdx.x];
-    float* out = c < d ? dq_w : dk_w;
-    if (out) out[c < d ? c : c - d] = s;
+    out[c] = s;
 }
 
-// Warps that share a token's heads: one where the tokens alone fill the GPU (148 SMs of 16 CTAs), more for
-// the few tokens of a serving step, down to one batch of rows a warp.
-int parts_of(int T, int heads, int d) {
-    const int rpw = 256 / d, most = (heads + rpw - 1) / rpw;
-    const int want = T ? (148 * 16 * kWarps + T - 1) / T : 1;
-    return want < 1 ? 1 : (want > most ? most : want);
+// Warps that share a token's heads, as a power of 2: one where the tokens alone fill the GPU (148 SMs of 16
+// warps, twice over), more for the few tokens of a serving step, down to one pass over a warp's rows.
+int parts_log_of(int T, int heads, int d) {
+    const int rpw = 512 / d;
+    int log = 0;
+    while (((int64_t)T << log) < 148 * 16 * 2 && (rpw << log) < heads) ++log;
+    return log;
 }
-// The backward's CTAs stay for the whole call: eight a SM.
-int bwd_ctas(int T) {
-    const int64_t c = ((int64_t)T + kWarps - 1) / kWarps;
-    return (int)(c < 148 * 8 ? c : 148 * 8);
+// The backward's CTAs stay for the whole call, four a SM, shared out by what a token costs either kind: its
+// passes of a warp, and about two more for the angles.
+void bwd_ctas(int T, int Hq, int Hk, int d, int* q, int* k) {
+    const int rpw = 512 / d;
+    const int64_t most = ((int64_t)T + kWarps - 1) / kWarps, all = 148 * 4;
+    const int64_t cq = (Hq + rpw - 1) / rpw + 2, ck = Hk ? (Hk + rpw - 1) / rpw + 2 : 0;
+    const int64_t nk = all * ck / (cq + ck), nq = all - nk;
+    *q = (int)(nq < most ? nq : most);
+    *k = (int)(nk < most ? nk : most);
 }
 
 template <class T, int D, bool APPEND>
 cudaError_t launch_fwd(const QkParams& p, cudaStream_t st) {
-    const int parts = parts_of(p.T, p.Hq > p.Hk ? p.Hq : p.Hk, D);
-    rope_fwd_kernel<T, D, APPEND><<<(unsigned)(((int64_t)p.T * parts + kWarps - 1) / kWarps), kThreads, 0, st>>>(p, parts);
+    const int log = parts_log_of(p.T, p.Hq > p.Hk ? p.Hq : p.Hk, D);
+    const unsigned ctas = (unsigned)((((int64_t)p.T << log) + kWarps - 1) / kWarps);
+    if (p.rope.interleaved) rope_fwd_kernel<T, D, true, APPEND><<<ctas, kThreads, 0, st>>>(p, log);
+    else rope_fwd_kernel<T, D, false, APPEND><<<ctas, kThreads, 0, st>>>(p, log);
     count_launch();
     return cudaGetLastError();
 }
 
 template <class T, int D>
 cudaError_t launch_bwd(const QkParams& p, float* dq_w, float* dk_w, void* dq, void* dk, cudaStream_t st) {
-    const int ctas = bwd_ctas(p.T);
-    if (ctas) {
-        rope_bwd_kernel<T, D><<<ctas, kThreads, 0, st>>>(p, static_cast<T*>(dq), static_cast<T*>(dk));
+    int nq, nk;
+    bwd_ctas(p.T, p.Hq, p.Hk, D, &nq, &nk);
+    if (nq + nk) {
+        if (p.rope.interleaved)
+            rope_bwd_kernel<T, D, true><<<nq + nk, kThreads, 0, st>>>(p, static_cast<T*>(dq), static_cast<T*>(dk), nq);
+        else
+            rope_bwd_kernel<T, D, false><<<nq + nk, kThreads, 0, st>>>(p, static_cast<T*>(dq), static_cast<T*>(dk), nq);
         count_launch();
     }
     if (p.partials) {
-        rope_dw_kernel<<<2 * D / 32, dim3(32, 32), 0, st>>>(p.partials, ctas, D, dq_w, dk_w);
+        rope_dw_kernel<<<dim3(D / 32, 2), dim3(32, 32), 0, st>>>(p.partials, nq, nk, D, dq_w, dk_w);
         count_launch();
     }
     return cudaGetLastError();
@@ -468,7 +547,11 @@ cudaError_t qk_norm_rope_fwd(const QkParams& p, int d, bool bf16, cudaStream_t s
     return d == 128 ? launch_fwd<float, 128, false>(p, st) : launch_fwd<float, 64, false>(p, st);
 }
 
-size_t qk_norm_rope_bwd_partials(int T, int d) { return (size_t)bwd_ctas(T) * 2 * d; }
+size_t qk_norm_rope_bwd_partials(int T, int Hq, int Hk, int d) {
+    int nq, nk;
+    bwd_ctas(T, Hq, Hk, d, &nq, &nk);
+    return (size_t)(nq + nk) * d;
+}
 
 cudaError_t qk_norm_rope_bwd(const QkParams& p, int d, bool bf16, void* dq, void* dk, float* dq_w, float* dk_w,
                              cudaStream_t st) {
