@@ -55,9 +55,11 @@ struct DecodeAttnParams {
     const void *k_cache, *v_cache;
     const int32_t *table, *context;
     void* o;
-    float* part;               // split contexts: [split][N * Hq][d + 2]
+    float* part;               // split contexts: [split][N * Hq][d], then [split][N * Hq][2]
     int64_t num_pages, max_pages, max_context, window;
     int64_t page_size;
+    uint32_t page_mul;         // pos / page_size = (pos * page_mul) >> page_shift
+    int page_shift;
     int N, Hq, Hk;
     int chunk, splits;         // tokens a split, splits a sequence
     float scale;

@@ -347,7 +347,7 @@ gdn_status gdn_kv_append(const gdn_kv_append_args* a, gdn_stream stream) {
 
 // Tokens a sequence can have, and read: the block table's reach and max_context, and of those the window's.
 static int64_t decode_max_context(const gdn_attn_decode_args* a) {
-    const int64_t limit = (int64_t(1) << 31) - 64;  // context_lens are 32-bit
+    const int64_t limit = (int64_t(1) << 31) - 4096;  // context_lens are 32-bit
     int64_t m = a->max_pages > limit / a->page_size ? limit : a->max_pages * a->page_size;
     if (a->max_context > 0 && a->max_context < m) m = a->max_context;
     return m;
