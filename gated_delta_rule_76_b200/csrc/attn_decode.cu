@@ -28,7 +28,6 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;    // tokens of a warp's tile
-constexpr int kStages = 3;   // tiles of a warp's ring: 2 in flight while one is read
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
     // with source size 0 nothing is read and the 16 bytes are zeros
@@ -77,8 +76,13 @@ __device__ __forceinline__ Context context_of(const DecodeAttnParams& p, int n) 
     return x;
 }
 
-template <int D>
+// A warp's ring holds kStages tiles, kStages - 1 of them on their way while one is read.  With up to 8 query
+// heads a group the registers allow three CTAs an SM, two stages each (64 KB at d = 128): 58.6 us for 256
+// sequences of 64 to 4500 tokens, against 64.1 us for two CTAs of three stages.  With more than 8 heads the registers
+// allow two.
+template <int D, bool ROWS16>
 struct Smem {
+    static constexpr int kStages = ROWS16 ? 3 : 2, kCtas = ROWS16 ? 2 : 3;
     static constexpr int kBox = kTile * 128;                 // 64 channels of a tile's rows, 128-byte swizzled
     static constexpr int kHalf = D / 64 * kBox;              // the tile's k (or v)
     static constexpr int kStage = 2 * kHalf;
@@ -89,8 +93,9 @@ struct Smem {
 
 // ROWS16: the group has more than 8 query heads; otherwise rows 8-15 of the products are padding.
 template <int D, bool PAGED16, bool ROWS16>
-__global__ void __launch_bounds__(kThreads, 2) decode_attn_kernel(const DecodeAttnParams p, float scale_log2) {
-    using S = Smem<D>;
+__global__ void __launch_bounds__(kThreads, Smem<D, ROWS16>::kCtas) decode_attn_kernel(const DecodeAttnParams p, float scale_log2) {
+    using S = Smem<D, ROWS16>;
+    constexpr int kStages = S::kStages;
     extern __shared__ __align__(1024) uint8_t smem[];
     // lets the joining kernel be set up while this one runs; it waits for this one's results itself
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const DecodeAttnParams p) 
 
 template <int D, bool PAGED16, bool ROWS16>
 cudaError_t launch(const DecodeAttnParams& p, cudaStream_t st) {
-    using S = Smem<D>;
+    using S = Smem<D, ROWS16>;
     auto kernel = decode_attn_kernel<D, PAGED16, ROWS16>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
     if (e != cudaSuccess) return e;
@@ -447,14 +452,15 @@ cudaError_t launch_d(DecodeAttnParams p, cudaStream_t st) {
 }  // namespace
 
 // Chunk length and number of chunks for contexts of up to `reach` tokens (and the tile before a window's
-// start).  Two CTAs fit on an SM; eight CTAs' worth of work an SM evens out ragged lengths, chunks of at most 1024
-// tokens keep a long sequence from being the tail, and at least 64 give every warp a tile.  The partial
+// start).  Eight CTAs' worth of work an SM evens out ragged lengths, chunks of at most 512 tokens keep a long
+// sequence from being the tail (256 sequences of 64 to 4500 tokens: 58.6 us; 59.1 us with 1024, 78 us with 256, whose
+// joins cost more), and at least 64 give every warp a tile.  The partial
 // results are bounded at 64 MB and 512 chunks, whatever the table's reach.
 void plan_decode_attn(int64_t N, int64_t Hq, int64_t Hk, int64_t reach, int* chunk, int* splits) {
     const int64_t units = N * Hk * ((Hq / Hk + 15) / 16);
     reach += kTile;
     int64_t c = (units * reach + 148 * 8 - 1) / (148 * 8);
-    c = c < 64 ? 64 : (c > 1024 ? 1024 : c);
+    c = c < 64 ? 64 : (c > 512 ? 512 : c);
     int64_t most = (int64_t(1) << 24) / (N * Hq * 130);
     most = most < 1 ? 1 : (most > 512 ? 512 : most);
     if (c * most < reach) c = (reach + most - 1) / most;
