@@ -76,14 +76,14 @@ struct AttnIO {
     int64_t window;            // 0: none
     float scale;
     void* o;                   // forward: out; backward: the forward's output
-    // the forward's cache: rows' log2-sum-exp2 of the scaled scores, tile-aligned [Hq][tiles][128], and
+    // the forward's cache: rows' -log2 sum exp2 of the scaled scores, tile-aligned [Hq][tiles][128], and
     // o - bf16(o) [T,Hq,d] (NULL in a forward that keeps none)
     float* lse;
     void* o_lo;
     // backward
     const void* grad_o;
     void *dq, *dk, *dv;
-    float* delta;              // [Hq][tiles][128]: rows' sum of grad_o .* o
+    float* delta;              // [Hq][tiles][128]: rows' -sum of grad_o .* o
     int* err;                  // device error word
     uint64_t wait_ns;          // limit of one bounded wait, 0: the default
 };

@@ -13,11 +13,14 @@
 // are the A operands of the second products; the row tiles in shared memory serve as K-major operands of
 // the first products and as MN-major ones of the second.
 //
-// The products of one item overlap the element-wise work of the next (issue order, dkdv):
+// Each CTA stays for the whole call and walks its units (a tile and a head), and their items (a pair of
+// tiles), as one stream: warp 8 copies, warp 9 issues the products, warps 0-7 do the element-wise work
+// (thread = row and half of the columns).  The products of one item overlap the element-wise work of the
+// next (issue order, dkdv):
 //     S(i) dP(i) | P(i) ready: dV(i) S(i+1) | dS(i) ready: dK(i) dP(i+1) | ...
 // so the tensor pipe runs dV(i), S(i+1) while dS(i) is formed, and dK(i), dP(i+1) while P(i+1) is.
-// 8 warps do the element-wise work (thread = row and half of the columns), one thread of a ninth issues every
-// copy and product; 192 KB of shared memory: the CTA's own two tiles, and two stages of the walked ones.
+// Shared memory (226 KB): the unit's own two tiles, three stages of the walked tile that S and the last product
+// read (a copy takes about as long as an item, and a stage is held for one and a half), two of the other.
 //
 // delta uses o with what its rounding left out (the cache's o_lo): row 0 of a sequence, where do . v - delta
 // cancels, keeps a gradient of 0.  ds and p are rounded to bf16 for the products, nothing else is.
@@ -29,22 +32,34 @@ namespace gdn {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 288;
+constexpr int kThreads = 320;
 constexpr int kElem = 256;  // element-wise threads
+constexpr int kCopyWarp = 8, kMmaWarp = 9;
 
 template <int D>
 struct BwdSmem {
     static constexpr uint32_t kTile = kRows * D * 2;
-    static constexpr uint32_t kOwn0 = 0, kOwn1 = kTile;                         // the CTA's own two tiles
-    static constexpr uint32_t kWalk = 2 * kTile;                                // [2 stages][2 tiles]
-    static constexpr uint32_t kStats = 6 * kTile;                               // dkdv: [2 stages][lse, delta][128]
-    static constexpr uint32_t kBar = kStats + 2 * 2 * kRows * 4;
-    static constexpr uint32_t kBytes = kBar + 128 + 1024;
-    static __device__ __forceinline__ uint32_t walk(int stage, int which) { return kWalk + (2 * stage + which) * kTile; }
+    static constexpr uint32_t kOwn0 = 0, kOwn1 = kTile;
+    static constexpr uint32_t kA = 2 * kTile, kB = 5 * kTile;  // [3] and [2] stages
+    static constexpr uint32_t kStats = 7 * kTile;              // dkdv: [2][-lse, -delta][128]
+    static constexpr uint32_t kBar = kStats + 2 * 1024;
+    static constexpr uint32_t kBytes = kBar + 160;             // the dynamic array starts on 1024 bytes
+    static __device__ __forceinline__ uint32_t a(int i) { return kA + (uint32_t)(i % 3) * kTile; }
+    static __device__ __forceinline__ uint32_t b(int i) { return kB + (uint32_t)(i & 1) * kTile; }
 };
+static_assert(BwdSmem<128>::kBytes <= 232448, "227 KB");
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_ACC0 = 256, TM_ACC1 = 384, TM_COLS = 512;
 
-enum BwdBar { B_OWN = 0, B_W0, B_W1, B_S, B_DP, B_X, B_DS, B_END, B_COUNT };
+enum BwdBar {
+    B_OWN = 0, B_OWN_FREE,      // own tiles landed; read for the last time
+    B_A, B_A_FREE = B_A + 3,    // stages of A
+    B_B = B_A_FREE + 3, B_B_FREE = B_B + 2,
+    B_S = B_B_FREE + 2, B_DP,   // products done
+    B_X, B_DS,                  // element-wise steps done (every thread arrives)
+    B_END,                      // the unit's accumulators are complete
+    B_COUNT
+};
+static_assert(B_COUNT * 8 <= 144, "barriers");
 
 struct BwdParams {
     AttnIO io;
@@ -52,24 +67,41 @@ struct BwdParams {
     float scale_log2;
 };
 
-__device__ __forceinline__ void setup(Ctx& cx, uint8_t* bars, const AttnIO& io, uint32_t*& tmem_slot) {
+// Barriers, tensor memory; false if the shared array does not start where the tiles need it.
+__device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const AttnIO& io, uint32_t*& tmem_slot) {
     cx.bars = reinterpret_cast<uint64_t*>(bars);
-    tmem_slot = reinterpret_cast<uint32_t*>(bars + 96);
-    cx.abort_flag = reinterpret_cast<volatile int*>(bars + 100);
+    tmem_slot = reinterpret_cast<uint32_t*>(bars + 144);
+    cx.abort_flag = reinterpret_cast<volatile int*>(bars + 148);
     cx.err = io.err;
     cx.wait_ns = io.wait_ns ? io.wait_ns : kWaitNs;
+    if (smem_u32(sm) & 1023u) {
+        if (threadIdx.x == 0) atomicOr(cx.err, 1);
+        return false;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i == B_X || i == B_DS ? kElem : 1);
         *cx.abort_flag = 0;
         mbar_fence_init();
     }
-    if (threadIdx.x >= kElem) {
+    if (threadIdx.x >> 5 == kMmaWarp) {
         tmem_alloc(tmem_slot, TM_COLS);
         tmem_relinquish();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    return true;
+}
+
+// After an expired wait: the copies still on their way land before the memory is given up.  owns, items: how
+// many of each were issued.
+__device__ __forceinline__ void drain(const Ctx& cx, int owns, int a_items, int b_items) {
+    if (!*cx.abort_flag) return;
+    if (owns) mbar_wait(cx.bars + B_OWN, (owns - 1) & 1, cx.wait_ns);
+    for (int i = a_items < 3 ? 0 : a_items - 3; i < a_items; ++i)
+        mbar_wait(cx.bars + B_A + i % 3, (i / 3) & 1, cx.wait_ns);
+    for (int i = b_items < 2 ? 0 : b_items - 2; i < b_items; ++i)
+        mbar_wait(cx.bars + B_B + (i & 1), (i >> 1) & 1, cx.wait_ns);
 }
 
 // D (+)= A B with A [128 x 128] bf16 in tensor memory as two halves of 32 columns, 64 columns apart, and
@@ -85,13 +117,32 @@ __device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uin
 }
 
 // 64 floats as bf16 pairs into 32 columns.
-__device__ __forceinline__ void st_half(uint32_t taddr, const float (&x)[64]) {
+__device__ __forceinline__ void st_half(uint32_t taddr, const f2 (&x)[32]) {
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
         uint32_t w[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(x[32 * q + 2 * e], x[32 * q + 2 * e + 1]);
+        for (int e = 0; e < 16; ++e) {
+            float lo, hi;
+            f2_get(x[16 * q + e], lo, hi);
+            w[e] = pack_bf16x2(lo, hi);
+        }
         tmem_st16(taddr + 16 * q, w);
+    }
+}
+// p = exp2(s c + nl) for a pair.
+__device__ __forceinline__ f2 exp_pair(uint32_t s0, uint32_t s1, f2 c, f2 nl) {
+    float a, b;
+    f2_get(f2_fma(f2_of(s0, s1), c, nl), a, b);
+    return f2_of(exp2_approx(a), exp2_approx(b));
+}
+// Columns outside [lo, hi] to 0.
+__device__ __forceinline__ void mask_pairs(f2 (&x)[32], int lo, int hi) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+        float a, b;
+        f2_get(x[c], a, b);
+        x[c] = f2_of(2 * c < lo || 2 * c > hi ? 0.f : a, 2 * c + 1 < lo || 2 * c + 1 > hi ? 0.f : b);
     }
 }
 
@@ -110,150 +161,188 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, int h, __nv_bfloat16* 
     }
 }
 
+// Items of a key tile's unit: G heads times the query tiles local .. last that see it.
+__device__ __forceinline__ int query_tiles(const Seq& sq, int window) {
+    const int key0 = sq.local * kRows, reach = sq.len - key0 - kRows;  // rows after the tile
+    const int last = reach < window - 1 ? sq.len - 1 : key0 + kRows - 1 + window - 1;
+    return last / kRows - sq.local + 1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
     using L = BwdSmem<D>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int hk = blockIdx.x % p.io.Hk, G = p.io.Hq / p.io.Hk;
-    Seq sq;
-    if (!find_tile(p.io.cu, p.io.nseq, p.io.T, (int)(blockIdx.x / p.io.Hk), sq)) return;
-    const int key0 = sq.local * kRows;
-    const int last_row = sq.len - 1 - key0 - (kRows - 1) < p.window - 1 ? sq.len - 1 : key0 + kRows - 1 + p.window - 1;
-    const int nq = last_row / kRows - sq.local + 1, m = G * nq;  // query tiles, items
+    const int G = p.io.Hq / p.io.Hk;
     Ctx cx;
     uint32_t* tmem_slot;
-    setup(cx, sm + L::kBar, p.io, tmem_slot);
+    if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
+    TileMap map(p.io.cu, p.io.nseq, p.io.T);
+    Seq sq;
+    int hk;
+    bool ok = true;
+    int gi = 0;  // items so far, over all units: the stages' and barriers' phases go by it
 
-    if (warp == 8) {
-        if ((tid & 31) == 0) {
-            int issued = 0, seen = 0;
-            auto load = [&](int it) {
-                const int head = hk * G + it / nq, tile = it % nq, st = it & 1;
-                uint64_t* bar = cx.bars + B_W0 + st;
-                mbar_arrive_expect_tx(bar, 2 * L::kTile + 2 * kRows * 4);
-                const int row = sq.begin + key0 + tile * kRows;
-                load_tile<D>(sb + L::walk(st, 0), &tm_q, bar, head, row);
-                load_tile<D>(sb + L::walk(st, 1), &tm_do, bar, head, row);
-                const int64_t stat = ((int64_t)head * p.tiles + sq.tile + tile) * kRows;
-                bulk_g2s(sb + L::kStats + st * 1024u, p.io.lse + stat, kRows * 4, bar);
-                bulk_g2s(sb + L::kStats + st * 1024u + 512u, p.io.delta + stat, kRows * 4, bar);
-                ++issued;
-            };
-            mbar_arrive_expect_tx(cx.bars + B_OWN, 2 * L::kTile);
-            load_tile<D>(sb + L::kOwn0, &tm_k, cx.bars + B_OWN, hk, sq.begin + key0);
-            load_tile<D>(sb + L::kOwn1, &tm_v, cx.bars + B_OWN, hk, sq.begin + key0);
-            load(0);
-            bool ok = wait_bar(cx, B_OWN, 0);
-            const bool own = ok;
-            if (ok && (ok = wait_bar(cx, B_W0, 0))) {
-                ++seen;
-                mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::walk(0, 0));
-                mma_commit(cx.bars + B_S);
-                mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::walk(0, 1));
-                mma_commit(cx.bars + B_DP);
+    if (warp == kCopyWarp) {
+        int owns = 0, a_items = 0, b_items = 0;  // issued
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, p.io.Hk, false, sq, hk);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const int key0 = sq.begin + sq.local * kRows, nq = query_tiles(sq, p.window), m = G * nq;
+            if ((tid & 31) == 0) {
+                for (int it = 0; ok && it < m; ++it, ++gi) {
+                    const int head = hk * G + it / nq, tile = it % nq;
+                    if (gi >= 3 && !(ok = wait_bar(cx, B_A_FREE + gi % 3, (gi / 3 - 1) & 1))) break;
+                    uint64_t* bar = cx.bars + B_A + gi % 3;
+                    mbar_arrive_expect_tx(bar, L::kTile);
+                    load_tile<D>(sb + L::a(gi), &tm_q, bar, head, key0 + tile * kRows);
+                    ++a_items;
+                    if (gi >= 2 && !(ok = wait_bar(cx, B_B_FREE + (gi & 1), ((gi >> 1) - 1) & 1))) break;
+                    bar = cx.bars + B_B + (gi & 1);
+                    mbar_arrive_expect_tx(bar, L::kTile + 2 * kRows * 4);
+                    load_tile<D>(sb + L::b(gi), &tm_do, bar, head, key0 + tile * kRows);
+                    const int64_t stat = ((int64_t)head * p.tiles + sq.tile + tile) * kRows;
+                    bulk_g2s(sb + L::kStats + (gi & 1) * 1024u, p.io.lse + stat, kRows * 4, bar);
+                    bulk_g2s(sb + L::kStats + (gi & 1) * 1024u + 512u, p.io.delta + stat, kRows * 4, bar);
+                    ++b_items;
+                    if (it == 0) {  // the first walked tiles need not wait for the unit before
+                        if (owns && !(ok = wait_bar(cx, B_OWN_FREE, (owns - 1) & 1))) break;
+                        mbar_arrive_expect_tx(cx.bars + B_OWN, 2 * L::kTile);
+                        load_tile<D>(sb + L::kOwn0, &tm_k, cx.bars + B_OWN, hk, key0);
+                        load_tile<D>(sb + L::kOwn1, &tm_v, cx.bars + B_OWN, hk, key0);
+                        ++owns;
+                    }
+                }
             }
-            for (int it = 0; ok && it < m; ++it) {
-                const int st = it & 1, nx = st ^ 1;
-                // the item before has left its stage: the next one may land there
-                if (it && !(ok = wait_bar(cx, B_END, (it - 1) & 1))) break;
-                if (it + 1 < m) load(it + 1);
-                if (!(ok = wait_bar(cx, B_X, it & 1))) break;
-                tc_fence_after();
-                mma_halves<D>(tbase + TM_ACC0, tbase + TM_S, sb + L::walk(st, 1), it > 0);
-                if (it + 1 < m) {
-                    if (!(ok = wait_bar(cx, B_W0 + nx, ((it + 1) >> 1) & 1))) break;
-                    ++seen;
-                    mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::walk(nx, 0));
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        if ((tid & 31) == 0) drain(cx, owns, a_items, b_items);
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        int owns = 0;
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, p.io.Hk, false, sq, hk);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const int m = G * query_tiles(sq, p.window);
+            if ((tid & 31) == 0) {
+                auto s_product = [&](int i) {
+                    mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::a(i));
                     mma_commit(cx.bars + B_S);
-                }
-                if (!(ok = wait_bar(cx, B_DS, it & 1))) break;
-                tc_fence_after();
-                mma_halves<D>(tbase + TM_ACC1, tbase + TM_DP, sb + L::walk(st, 0), it > 0);
-                mma_commit(cx.bars + B_END);
-                if (it + 1 < m) {
-                    mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::walk(nx, 1));
+                };
+                auto dp_product = [&](int i, bool last) {
+                    mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::b(i));
                     mma_commit(cx.bars + B_DP);
+                    if (last) mma_commit(cx.bars + B_OWN_FREE);
+                };
+                ok = wait_bar(cx, B_OWN, owns & 1) && wait_bar(cx, B_A + gi % 3, (gi / 3) & 1);
+                ++owns;
+                if (ok) s_product(gi);
+                if (ok && (ok = wait_bar(cx, B_B + (gi & 1), (gi >> 1) & 1))) dp_product(gi, m == 1);
+                for (int it = 0; ok && it < m; ++it, ++gi) {
+                    if (!(ok = wait_bar(cx, B_X, gi & 1))) break;
+                    tc_fence_after();
+                    mma_halves<D>(tbase + TM_ACC0, tbase + TM_S, sb + L::b(gi), it > 0);
+                    if (it + 1 < m) {
+                        if (!(ok = wait_bar(cx, B_A + (gi + 1) % 3, ((gi + 1) / 3) & 1))) break;
+                        s_product(gi + 1);  // runs after dV, so it may write over P
+                    }
+                    if (!(ok = wait_bar(cx, B_DS, gi & 1))) break;
+                    tc_fence_after();
+                    mma_halves<D>(tbase + TM_ACC1, tbase + TM_DP, sb + L::a(gi), it > 0);
+                    mma_commit(cx.bars + B_A_FREE + gi % 3);
+                    mma_commit(cx.bars + B_B_FREE + (gi & 1));
+                    if (it + 1 == m) mma_commit(cx.bars + B_END);
+                    else {
+                        if (!(ok = wait_bar(cx, B_B + ((gi + 1) & 1), ((gi + 1) >> 1) & 1))) break;
+                        dp_product(gi + 1, it + 2 == m);
+                    }
                 }
             }
-            // after an expired wait: the copies still on their way land before the memory is given up
-            if (!own) mbar_wait(cx.bars + B_OWN, 0, cx.wait_ns);
-            for (; seen < issued; ++seen) mbar_wait(cx.bars + B_W0 + (seen & 1), (seen >> 1) & 1, cx.wait_ns);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         __syncwarp();
     } else {
         const int lane = tid & 127, h = tid >> 7;
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-        const int key = key0 + lane;  // within the sequence
-        bool ok = true;
-        for (int it = 0; it < m; ++it) {
-            const int st = it & 1, row0 = key0 + (it % nq) * kRows + 64 * h;  // row of this thread's first column
-            const float* lse = reinterpret_cast<const float*>(sm + L::kStats + st * 1024) + 64 * h;
-            const float* delta = lse + kRows;
-            if (!(ok = wait_warp(cx, B_W0 + st, (it >> 1) & 1))) break;  // the statistics have landed
-            if (!(ok = wait_warp(cx, B_S, it & 1))) break;
-            tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32(tl + TM_S + 64 * h, s[0]);
-            tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
-            tmem_ld_wait();
-            float x[64];
+        const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
+        int units = 0;
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, p.io.Hk, false, sq, hk);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const int key0 = sq.local * kRows, nq = query_tiles(sq, p.window), m = G * nq;
+            const int key = key0 + lane;  // within the sequence
+            for (int it = 0, tile = 0; it < m; ++it, ++gi, tile = tile + 1 == nq ? 0 : tile + 1) {
+                const int q0 = key0 + tile * kRows;
+                const float* nlse = reinterpret_cast<const float*>(sm + L::kStats + (gi & 1) * 1024) + 64 * h;
+                const float* ndelta = nlse + kRows;
+                if (!(ok = wait_warp(cx, B_B + (gi & 1), (gi >> 1) & 1))) break;  // the statistics have landed
+                if (!(ok = wait_warp(cx, B_S, gi & 1))) break;
+                tc_fence_after();
+                uint32_t s[2][32];
+                tmem_ld32(tl + TM_S + 64 * h, s[0]);
+                tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
+                tmem_ld_wait();
+                f2 x[32];
 #pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 l4 = *reinterpret_cast<const float4*>(lse + c);
-                const float ls[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[c + e] = exp2_approx(fmaf(__uint_as_float(s[(c + e) >> 5][(c + e) & 31]), p.scale_log2, -ls[e]));
-            }
-            // rows before the key, past its window or past the sequence
-            const int q0 = key0 + (it % nq) * kRows;
-            const bool tail = q0 + kRows > sq.len;
-            if (q0 == key0 || tail || q0 + kRows - 1 - key0 >= p.window) {
-                const int lo = key - row0;  // first visible column
-                const int hi = min(p.window - 1 < sq.len ? key + p.window - 1 : sq.len - 1, sq.len - 1) - row0;
-#pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (c < lo || c > hi) x[c] = 0.f;
-            }
-            st_half(tl + TM_S + 64 * h, x);
-            if (tail) {
-                // rows past the sequence have weight 0, but 0 * NaN is not 0; both first products have read them
-                if (!(ok = wait_warp(cx, B_DP, it & 1))) break;
-                if (lane >= sq.len - q0) zero_row<D>(sm + L::walk(st, h), lane);
-                fence_async_shared();
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(cx.bars + B_X);
-            if (!(ok = wait_warp(cx, B_DP, it & 1))) break;
-            tc_fence_after();
-            tmem_ld32(tl + TM_DP + 64 * h, s[0]);
-            tmem_ld32(tl + TM_DP + 64 * h + 32, s[1]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 d4 = *reinterpret_cast<const float4*>(delta + c);
-                const float de[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float t = x[c + e] * (__uint_as_float(s[(c + e) >> 5][(c + e) & 31]) - de[e]);
-                    x[c + e] = x[c + e] == 0.f ? 0.f : t;  // a row past the sequence may hold anything
+                for (int c = 0; c < 32; c += 2) {
+                    const float4 l4 = *reinterpret_cast<const float4*>(nlse + 2 * c);
+                    x[c] = exp_pair(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31], scale2, f2_of(l4.x, l4.y));
+                    x[c + 1] = exp_pair(s[c >> 4][(2 * c + 2) & 31], s[c >> 4][(2 * c + 3) & 31], scale2, f2_of(l4.z, l4.w));
                 }
+                // rows before the key, past its window or past the sequence
+                const bool tail = q0 + kRows > sq.len;
+                const bool masked = tile == 0 || tail || q0 + kRows - 1 - key0 >= p.window;
+                if (masked) {
+                    const int row0 = q0 + 64 * h;
+                    mask_pairs(x, key - row0, min(p.window - 1 < sq.len ? key + p.window - 1 : sq.len - 1, sq.len - 1) - row0);
+                }
+                st_half(tl + TM_S + 64 * h, x);
+                if (tail) {
+                    // rows past the sequence have weight 0, but 0 * NaN is not 0; both first products have read them
+                    if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
+                    if (lane >= sq.len - q0) zero_row<D>(sm + (h ? L::b(gi) : L::a(gi)), lane);
+                    fence_async_shared();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(cx.bars + B_X);
+                if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
+                tc_fence_after();
+                tmem_ld32(tl + TM_DP + 64 * h, s[0]);
+                tmem_ld32(tl + TM_DP + 64 * h + 32, s[1]);
+                tmem_ld_wait();
+                if (masked) {  // where the weight is 0, do . v may be anything
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        float a, b;
+                        f2_get(x[c], a, b);
+                        if (a == 0.f) s[c >> 4][(2 * c) & 31] = 0u;
+                        if (b == 0.f) s[c >> 4][(2 * c + 1) & 31] = 0u;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 32; c += 2) {
+                    const float4 d4 = *reinterpret_cast<const float4*>(ndelta + 2 * c);
+                    x[c] = f2_mul(x[c], f2_add(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), f2_of(d4.x, d4.y)));
+                    x[c + 1] = f2_mul(x[c + 1],
+                                      f2_add(f2_of(s[c >> 4][(2 * c + 2) & 31], s[c >> 4][(2 * c + 3) & 31]), f2_of(d4.z, d4.w)));
+                }
+                st_half(tl + TM_DP + 64 * h, x);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(cx.bars + B_DS);
             }
-            st_half(tl + TM_DP + 64 * h, x);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(cx.bars + B_DS);
-            if (it && !(ok = wait_warp(cx, B_END, (it - 1) & 1))) break;  // long past; keeps its phase in step
-        }
-        if (ok && wait_warp(cx, B_END, (m - 1) & 1)) {
+            if (!ok || !(ok = wait_warp(cx, B_END, units & 1))) break;
+            ++units;
             tc_fence_after();
+            // the next unit's first product into these accumulators waits for its P, which follows this
             const int64_t at = ((int64_t)(sq.begin + key) * p.io.Hk + hk) * D;
             store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, 1.f, key < sq.len);
             store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, p.io.scale, key < sq.len);
@@ -262,7 +351,7 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tbase, TM_COLS);
+    if (warp == kMmaWarp) tmem_dealloc(tbase, TM_COLS);
 }
 
 template <int D>
@@ -270,119 +359,159 @@ __global__ void __launch_bounds__(kThreads, 1)
 attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do, const BwdParams p) {
     using L = BwdSmem<D>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int head = blockIdx.x % p.io.Hq, hk = head / (p.io.Hq / p.io.Hk);
-    Seq sq;
-    if (!find_tile(p.io.cu, p.io.nseq, p.io.T, p.tiles - 1 - (int)(blockIdx.x / p.io.Hq), sq)) return;
-    const int row0 = sq.local * kRows;
-    const int lo = max(0, row0 - p.window + 1) / kRows, hi = sq.local, m = hi - lo + 1;
+    const int G = p.io.Hq / p.io.Hk;
     Ctx cx;
     uint32_t* tmem_slot;
-    setup(cx, sm + L::kBar, p.io, tmem_slot);
+    if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
+    TileMap map(p.io.cu, p.io.nseq, p.io.T);
+    Seq sq;
+    int head;
+    bool ok = true;
+    int gi = 0;
+    // key tiles of a unit, from the diagonal down to the window's edge
+    auto key_tiles = [&]() { return sq.local - max(0, sq.local * kRows - p.window + 1) / kRows + 1; };
 
-    if (warp == 8) {
-        if ((tid & 31) == 0) {
-            int issued = 0, seen = 0;
-            auto load = [&](int it) {
-                const int st = it & 1, row = sq.begin + (hi - it) * kRows;
-                uint64_t* bar = cx.bars + B_W0 + st;
-                mbar_arrive_expect_tx(bar, 2 * L::kTile);
-                load_tile<D>(sb + L::walk(st, 0), &tm_k, bar, hk, row);
-                load_tile<D>(sb + L::walk(st, 1), &tm_v, bar, hk, row);
-                ++issued;
-            };
-            mbar_arrive_expect_tx(cx.bars + B_OWN, 2 * L::kTile);
-            load_tile<D>(sb + L::kOwn0, &tm_q, cx.bars + B_OWN, head, sq.begin + row0);
-            load_tile<D>(sb + L::kOwn1, &tm_do, cx.bars + B_OWN, head, sq.begin + row0);
-            load(0);
-            bool ok = wait_bar(cx, B_OWN, 0);
-            const bool own = ok;
-            if (ok && (ok = wait_bar(cx, B_W0, 0))) {
-                ++seen;
-                mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::walk(0, 0));
-                mma_commit(cx.bars + B_S);
-                mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::walk(0, 1));
-                mma_commit(cx.bars + B_DP);
+    if (warp == kCopyWarp) {
+        int owns = 0, a_items = 0, b_items = 0;  // issued
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, p.io.Hq, true, sq, head);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const int m = key_tiles(), hk = head / G, row0 = sq.begin + sq.local * kRows;
+            if ((tid & 31) == 0) {
+                for (int it = 0; ok && it < m; ++it, ++gi) {
+                    const int row = row0 - it * kRows;
+                    if (gi >= 3 && !(ok = wait_bar(cx, B_A_FREE + gi % 3, (gi / 3 - 1) & 1))) break;
+                    uint64_t* bar = cx.bars + B_A + gi % 3;
+                    mbar_arrive_expect_tx(bar, L::kTile);
+                    load_tile<D>(sb + L::a(gi), &tm_k, bar, hk, row);
+                    ++a_items;
+                    if (gi >= 2 && !(ok = wait_bar(cx, B_B_FREE + (gi & 1), ((gi >> 1) - 1) & 1))) break;
+                    bar = cx.bars + B_B + (gi & 1);
+                    mbar_arrive_expect_tx(bar, L::kTile);
+                    load_tile<D>(sb + L::b(gi), &tm_v, bar, hk, row);
+                    ++b_items;
+                    if (it == 0) {
+                        if (owns && !(ok = wait_bar(cx, B_OWN_FREE, (owns - 1) & 1))) break;
+                        mbar_arrive_expect_tx(cx.bars + B_OWN, 2 * L::kTile);
+                        load_tile<D>(sb + L::kOwn0, &tm_q, cx.bars + B_OWN, head, row0);
+                        load_tile<D>(sb + L::kOwn1, &tm_do, cx.bars + B_OWN, head, row0);
+                        ++owns;
+                    }
+                }
             }
-            for (int it = 0; ok && it < m; ++it) {
-                const int st = it & 1, nx = st ^ 1;
-                if (it && !(ok = wait_bar(cx, B_END, (it - 1) & 1))) break;
-                if (it + 1 < m) load(it + 1);
-                if (!(ok = wait_bar(cx, B_X, it & 1))) break;  // S(it) is in registers
-                if (it + 1 < m) {
-                    if (!(ok = wait_bar(cx, B_W0 + nx, ((it + 1) >> 1) & 1))) break;
-                    ++seen;
-                    tc_fence_after();
-                    mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::walk(nx, 0));
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        }
+        if ((tid & 31) == 0) drain(cx, owns, a_items, b_items);
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        int owns = 0;
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, p.io.Hq, true, sq, head);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const int m = key_tiles();
+            if ((tid & 31) == 0) {
+                auto s_product = [&](int i) {
+                    mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::a(i));
                     mma_commit(cx.bars + B_S);
-                }
-                if (!(ok = wait_bar(cx, B_DS, it & 1))) break;
-                tc_fence_after();
-                mma_halves<D>(tbase + TM_ACC0, tbase + TM_DP, sb + L::walk(st, 0), it > 0);
-                mma_commit(cx.bars + B_END);
-                if (it + 1 < m) {
-                    mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::walk(nx, 1));
+                };
+                auto dp_product = [&](int i, bool last) {
+                    mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::b(i));
                     mma_commit(cx.bars + B_DP);
+                    mma_commit(cx.bars + B_B_FREE + (i & 1));
+                    if (last) mma_commit(cx.bars + B_OWN_FREE);
+                };
+                ok = wait_bar(cx, B_OWN, owns & 1) && wait_bar(cx, B_A + gi % 3, (gi / 3) & 1);
+                ++owns;
+                if (ok) s_product(gi);
+                if (ok && (ok = wait_bar(cx, B_B + (gi & 1), (gi >> 1) & 1))) dp_product(gi, m == 1);
+                for (int it = 0; ok && it < m; ++it, ++gi) {
+                    if (!(ok = wait_bar(cx, B_X, gi & 1))) break;  // S is in registers
+                    if (it + 1 < m) {
+                        if (!(ok = wait_bar(cx, B_A + (gi + 1) % 3, ((gi + 1) / 3) & 1))) break;
+                        tc_fence_after();
+                        s_product(gi + 1);
+                    }
+                    if (!(ok = wait_bar(cx, B_DS, gi & 1))) break;
+                    tc_fence_after();
+                    mma_halves<D>(tbase + TM_ACC0, tbase + TM_DP, sb + L::a(gi), it > 0);
+                    mma_commit(cx.bars + B_A_FREE + gi % 3);
+                    if (it + 1 == m) mma_commit(cx.bars + B_END);
+                    else {
+                        if (!(ok = wait_bar(cx, B_B + ((gi + 1) & 1), ((gi + 1) >> 1) & 1))) break;
+                        dp_product(gi + 1, it + 2 == m);
+                    }
                 }
             }
-            if (!own) mbar_wait(cx.bars + B_OWN, 0, cx.wait_ns);
-            for (; seen < issued; ++seen) mbar_wait(cx.bars + B_W0 + (seen & 1), (seen >> 1) & 1, cx.wait_ns);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         }
         __syncwarp();
     } else {
         const int lane = tid & 127, h = tid >> 7;
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
-        const int row = row0 + lane;
-        const int64_t stat = ((int64_t)head * p.tiles + sq.tile) * kRows + lane;
-        const float lse = __ldg(p.io.lse + stat), delta = __ldg(p.io.delta + stat);
-        bool ok = true;
-        for (int it = 0; it < m; ++it) {
-            const int key0 = (hi - it) * kRows;
-            if (!(ok = wait_warp(cx, B_S, it & 1))) break;
-            tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32(tl + TM_S + 64 * h, s[0]);
-            tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
-            tmem_ld_wait();
-            tc_fence_before();
-            mbar_arrive(cx.bars + B_X);
-            float x[64];
+        const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
+        int units = 0;
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, p.io.Hq, true, sq, head);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const int m = key_tiles(), row0 = sq.local * kRows, row = row0 + lane;
+            const int64_t stat = ((int64_t)head * p.tiles + sq.tile) * kRows + lane;
+            const float nlse = __ldg(p.io.lse + stat), ndelta = __ldg(p.io.delta + stat);
+            const f2 nlse2 = f2_of(nlse, nlse), ndelta2 = f2_of(ndelta, ndelta);
+            for (int it = 0; it < m; ++it, ++gi) {
+                const int key0 = row0 - it * kRows;
+                if (!(ok = wait_warp(cx, B_S, gi & 1))) break;
+                tc_fence_after();
+                uint32_t s[2][32];
+                tmem_ld32(tl + TM_S + 64 * h, s[0]);
+                tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
+                tmem_ld_wait();
+                tc_fence_before();
+                mbar_arrive(cx.bars + B_X);
+                f2 x[32];
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-                x[c] = exp2_approx(fmaf(__uint_as_float(s[c >> 5][c & 31]), p.scale_log2, -lse));
-            // keys after the row or out of its window
-            if (it == 0 || key0 <= row0 + kRows - 1 - p.window) {
-                const int last = row - key0 - 64 * h, gone = last - p.window;
+                for (int c = 0; c < 32; ++c) x[c] = exp_pair(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31], scale2, nlse2);
+                // keys after the row or out of its window
+                const bool masked = it == 0 || key0 <= row0 + kRows - 1 - p.window;
+                if (masked) {
+                    const int last = row - key0 - 64 * h;
+                    mask_pairs(x, last - p.window + 1, last);
+                }
+                if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
+                tc_fence_after();
+                tmem_ld32(tl + TM_DP + 64 * h, s[0]);
+                tmem_ld32(tl + TM_DP + 64 * h + 32, s[1]);
+                tmem_ld_wait();
+                if (masked) {  // where the weight is 0, do . v may be anything
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (c > last || c <= gone) x[c] = 0.f;
-            }
-            if (!(ok = wait_warp(cx, B_DP, it & 1))) break;
-            tc_fence_after();
-            tmem_ld32(tl + TM_DP + 64 * h, s[0]);
-            tmem_ld32(tl + TM_DP + 64 * h + 32, s[1]);
-            tmem_ld_wait();
+                    for (int c = 0; c < 32; ++c) {
+                        float a, b;
+                        f2_get(x[c], a, b);
+                        if (a == 0.f) s[c >> 4][(2 * c) & 31] = 0u;
+                        if (b == 0.f) s[c >> 4][(2 * c + 1) & 31] = 0u;
+                    }
+                }
 #pragma unroll
-            for (int c = 0; c < 64; ++c) {
-                const float t = x[c] * (__uint_as_float(s[c >> 5][c & 31]) - delta);
-                x[c] = x[c] == 0.f ? 0.f : t;  // a key past the sequence may hold anything
+                for (int c = 0; c < 32; ++c)
+                    x[c] = f2_mul(x[c], f2_add(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), ndelta2));
+                st_half(tl + TM_DP + 64 * h, x);
+                if (it == 0 && sq.len - key0 < kRows) {
+                    // K's rows past the sequence: their ds is 0, but 0 * NaN is not; S and dP are done with them
+                    if (h == 0 && lane >= sq.len - key0) zero_row<D>(sm + L::a(gi), lane);
+                    fence_async_shared();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(cx.bars + B_DS);
             }
-            st_half(tl + TM_DP + 64 * h, x);
-            if (it == 0 && sq.len - key0 < kRows) {
-                // K's rows past the sequence: their ds is 0, but 0 * NaN is not; S(0) and dP(0) are done with them
-                if (h == 0 && lane >= sq.len - key0) zero_row<D>(sm + L::walk(0, 0), lane);
-                fence_async_shared();
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(cx.bars + B_DS);
-            if (it && !(ok = wait_warp(cx, B_END, (it - 1) & 1))) break;
-        }
-        if (ok && wait_warp(cx, B_END, (m - 1) & 1)) {
+            if (!ok || !(ok = wait_warp(cx, B_END, units & 1))) break;
+            ++units;
             tc_fence_after();
             const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + head) * D;
             store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dq) + at, p.io.scale, row < sq.len);
@@ -391,17 +520,18 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tbase, TM_COLS);
+    if (warp == kMmaWarp) tmem_dealloc(tbase, TM_COLS);
 }
 
-// delta = do . (o + o_lo) of every row, tile-aligned like lse (0 for a tile's rows past its sequence).
+// -delta = -do . (o + o_lo) of every row, tile-aligned like lse (0 for a tile's rows past its sequence).
 // D / 8 lanes a row, 8 channels each.  HBM bound: three reads of 2 bytes a channel.
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int tiles) {
     constexpr int LANES = D / 8, RPP = 256 / LANES;
     Seq sq;
     const int head = blockIdx.x % io.Hq;
-    if (!find_tile(io.cu, io.nseq, io.T, (int)(blockIdx.x / io.Hq), sq)) return;
+    TileMap map(io.cu, io.nseq, io.T);
+    if (!map.find((int)(blockIdx.x / io.Hq), false, sq)) return;
     const int c0 = (threadIdx.x % LANES) * 8;
     const int row0 = sq.local * kRows;
 #pragma unroll
@@ -423,7 +553,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int ti
         }
 #pragma unroll
         for (int o = LANES / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (c0 == 0) io.delta[((int64_t)head * tiles + sq.tile) * kRows + r] = sum;
+        if (c0 == 0) io.delta[((int64_t)head * tiles + sq.tile) * kRows + r] = -sum;
     }
 }
 
@@ -438,10 +568,10 @@ cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st)
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BwdSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    attn_dkdv_kernel<D><<<k_tiles, kThreads, BwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], maps[3], p);
+    attn_dkdv_kernel<D><<<k_tiles < 148 ? k_tiles : 148, kThreads, BwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], maps[3], p);
     count_launch();
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_dq_kernel<D><<<q_tiles, kThreads, BwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], maps[3], p);
+    attn_dq_kernel<D><<<q_tiles < 148 ? q_tiles : 148, kThreads, BwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], maps[3], p);
     count_launch();
     return cudaGetLastError();
 }

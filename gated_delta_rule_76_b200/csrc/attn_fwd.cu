@@ -50,8 +50,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const int tid = threadIdx.x, warp = tid >> 5;
     const int head = blockIdx.x % p.io.Hq;
     Seq sq;
-    // later tiles first: they see the most keys
-    if (!find_tile(p.io.cu, p.io.nseq, p.io.T, p.tiles - 1 - (int)(blockIdx.x / p.io.Hq), sq)) return;
+    TileMap map(p.io.cu, p.io.nseq, p.io.T);
+    if (!map.find((int)(blockIdx.x / p.io.Hq), true, sq)) return;
     const int hk = head / (p.io.Hq / p.io.Hk);
     const int row0 = sq.local * kRows;  // first row, within the sequence
     const int first_key = max(0, row0 - p.window + 1);
@@ -228,7 +228,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
             }
             // every row of the tile, so that the backward's copies of it read no uninitialised memory
-            if (SAVE) p.io.lse[((int64_t)head * p.tiles + sq.tile) * kRows + tid] = live ? m + log2f(l) : 0.f;
+            if (SAVE) p.io.lse[((int64_t)head * p.tiles + sq.tile) * kRows + tid] = live ? -(m + log2f(l)) : 0.f;
         }
     }
     tc_fence_before();

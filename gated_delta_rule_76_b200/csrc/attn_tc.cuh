@@ -2,8 +2,8 @@
 // waits, TMA loads of row tiles, and the product loops over their shared-memory tiles.
 //
 // Tiles: every sequence is cut into tiles of 128 rows from its own start, and the tiles of all
-// sequences are numbered in order; T / 128 + nseq bounds their number on the host, and a CTA finds
-// its sequence by a scan over cu_seqlens, 32 sequences a step.  A tile's rows past the end of its
+// sequences are numbered in order; T / 128 + nseq bounds their number on the host.  CTAs stay for the whole
+// call and find their units of work themselves (TileMap), from cu_seqlens, which the host does not see.  A tile's rows past the end of its
 // sequence belong to others (or to nobody): they are loaded, never stored, and kept out of every
 // sum (masked scores; zeroed rows of operands that a zero weight would multiply, since 0 * NaN is
 // not 0).
@@ -30,38 +30,96 @@ struct Seq {
     int tile, local;  // global tile number, tile within the sequence
 };
 
-// Warp-collective: the sequence and local tile of global tile `g`, false past the last one.
-__device__ __forceinline__ bool find_tile(const int32_t* cu, int nseq, int T, int g, Seq& out) {
-    const int lane = threadIdx.x & 31;
-    int before = 0;
-    for (int s0 = 0; s0 < nseq; s0 += 32) {
-        const int s = s0 + lane;
-        int b = 0, e = 0;
+// The map from a CTA's units of work to tiles, one per warp (every call is warp-collective).  With up to 32
+// sequences the tiles come in descending order of their work: a tile of a causal sequence of t tiles has
+// 1, 2, .. or t tiles to look at, one tile of each (a window caps the larger ones, which keeps the order), so
+// the r-th heaviest is found by counting.  With more sequences they come in the sequences' order.
+struct TileMap {
+    const int32_t* cu;
+    int nseq, T;
+    int b, e, t, first;  // up to 32 sequences: this lane's one, its tiles and the first of them
+    int total;           // tiles
+
+    __device__ __forceinline__ void bounds(int s, int& x, int& y) const {
+        x = y = 0;
         if (s < nseq) {
-            b = min(max(__ldg(cu + s), 0), T);
-            e = min(max(__ldg(cu + s + 1), b), T);
+            x = min(max(__ldg(cu + s), 0), T);
+            y = min(max(__ldg(cu + s + 1), x), T);
         }
-        const int tiles = (e - b + kRows - 1) / kRows;
-        int incl = tiles;
+    }
+    static __device__ __forceinline__ int scan(int x) {  // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += x;
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if ((threadIdx.x & 31) >= o) x += y;
         }
-        const int start = before + incl - tiles;
-        const uint32_t hit = __ballot_sync(0xffffffffu, g >= start && g < start + tiles);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            out.begin = __shfl_sync(0xffffffffu, b, src);
-            out.len = __shfl_sync(0xffffffffu, e, src) - out.begin;
-            out.local = g - __shfl_sync(0xffffffffu, start, src);
-            out.tile = g;
+        return x;
+    }
+    __device__ __forceinline__ TileMap(const int32_t* cu_, int nseq_, int T_) : cu(cu_), nseq(nseq_), T(T_) {
+        total = 0;
+        for (int s0 = 0; s0 < nseq; s0 += 32) {
+            bounds(s0 + (threadIdx.x & 31), b, e);
+            t = (e - b + kRows - 1) / kRows;
+            const int incl = scan(t);
+            first = incl - t;
+            total += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    __device__ __forceinline__ void take(Seq& out, int src, int local) const {
+        out.begin = __shfl_sync(0xffffffffu, b, src);
+        out.len = __shfl_sync(0xffffffffu, e, src) - out.begin;
+        out.local = local;
+        out.tile = __shfl_sync(0xffffffffu, first, src) + local;
+    }
+    // Tile `rank` of the order; up: the work grows with the tile's place in its sequence (query tiles, which
+    // see the keys before them), else it falls (key tiles).  False past the last one.
+    __device__ __forceinline__ bool find(int rank, bool up, Seq& out) {
+        if (rank >= total) return false;
+        const int lane = threadIdx.x & 31;
+        if (nseq <= 32) {
+            // the largest work x that more than `rank` tiles reach
+            int lo = 1, hi = __reduce_max_sync(0xffffffffu, t);
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if ((int)__reduce_add_sync(0xffffffffu, max(0, t - mid + 1)) > rank) lo = mid;
+                else hi = mid - 1;
+            }
+            const int among = rank - (int)__reduce_add_sync(0xffffffffu, max(0, t - lo));
+            const uint32_t have = __ballot_sync(0xffffffffu, t >= lo);
+            const bool me = t >= lo && __popc(have & ((1u << lane) - 1u)) == among;
+            const int src = __ffs(__ballot_sync(0xffffffffu, me)) - 1;
+            const int n = __shfl_sync(0xffffffffu, t, src);
+            take(out, src, up ? lo - 1 : n - lo);
             return true;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        const int g = up ? total - 1 - rank : rank;
+        int before = 0;
+        for (int s0 = 0;; s0 += 32) {
+            bounds(s0 + lane, b, e);
+            t = (e - b + kRows - 1) / kRows;
+            const int incl = scan(t);
+            first = before + incl - t;
+            const uint32_t hit = __ballot_sync(0xffffffffu, g >= first && g < first + t);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                take(out, src, g - __shfl_sync(0xffffffffu, first, src));
+                return true;
+            }
+            before += __shfl_sync(0xffffffffu, incl, 31);
+        }
     }
-    return false;
-}
+    // Unit k of this CTA's share of `heads` times the tiles: rows of the grid's width in the order above,
+    // every second one backwards, so that the CTAs' sums even out.  0: unit found, 1: none in this row, 2: no more.
+    __device__ __forceinline__ int unit(int k, int heads, bool up, Seq& sq, int& head) {
+        const int64_t at = (int64_t)k * gridDim.x;
+        if (at >= (int64_t)total * heads) return 2;
+        const int64_t u = at + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        if (u >= (int64_t)total * heads) return 1;
+        const uint32_t rank = (uint32_t)u / (uint32_t)heads;  // u < 2^31: the host checks
+        head = (int)((uint32_t)u - rank * (uint32_t)heads);
+        return find((int)rank, up, sq) ? 0 : 2;
+    }
+};
 
 struct Ctx {
     uint64_t* bars;
@@ -130,6 +188,37 @@ __device__ __forceinline__ void zero_row(uint8_t* tile, int row) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) p[i] = make_uint4(0u, 0u, 0u, 0u);
     }
+}
+
+// ---- pairs of fp32 in one 64-bit register ------------------------------------------------------
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 f2_of(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ f2 f2_of(uint32_t lo, uint32_t hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ void f2_get(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 f2_add(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
