@@ -181,7 +181,7 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t* tmem_slot;
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
-    TileMap map(p.io.cu, p.io.nseq, p.io.T);
+    TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
     Seq sq;
     int hk;
     bool ok = true;
@@ -367,7 +367,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint32_t* tmem_slot;
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
-    TileMap map(p.io.cu, p.io.nseq, p.io.T);
+    TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
     Seq sq;
     int head;
     bool ok = true;
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int ti
     constexpr int LANES = D / 8, RPP = 256 / LANES;
     Seq sq;
     const int head = blockIdx.x % io.Hq;
-    TileMap map(io.cu, io.nseq, io.T);
+    TileMap<kRows> map(io.cu, io.nseq, io.T);
     if (!map.find((int)(blockIdx.x / io.Hq), false, sq)) return;
     const int c0 = (threadIdx.x % LANES) * 8;
     const int row0 = sq.local * kRows;

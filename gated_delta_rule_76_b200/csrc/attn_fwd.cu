@@ -1,18 +1,24 @@
 // Causal softmax attention over packed sequences, forward, on the 5th-generation tensor cores.
 //
-// One CTA per (128 query rows, query head), keys in tiles of 128 from the diagonal down to the
-// window's edge (the diagonal first: every row then has a finite maximum from the first tile on).
+// A unit of work is two tiles of 128 query rows that look at the same keys: the same rows of two query heads
+// of one key head (PAIR_HEADS, where the group is even: their key tiles are the same), or else 256 rows of one
+// head.  Keys come in tiles of 128 from the diagonal down to the window's edge (the diagonal first: every row
+// then has a finite maximum from the first tile on).  For each of the two:
 //     S = Q K^T            tcgen05, Q and K row tiles in shared memory, 128 columns of tensor memory
-//     P = exp2(S c - m)    thread t owns row t: c = scale log2(e), running reference m and sum l
+//     P = exp2(S c - m)    a thread a row: c = scale log2(e), running reference m and sum l
 //     O += P V             tcgen05, P as bf16 over S's columns (A in tensor memory), V as MN-major B
 // m is not moved for every new maximum: any reference within 2^8 of it serves as well (p stays below
 // 2^8, sums stay fp32, and bf16's relative rounding does not depend on it), so the O accumulator is
 // rescaled only when a row's maximum has outgrown m by more than 8.
 // P is rounded to bf16 because that is what the tensor cores multiply with bf16 V; l sums the unrounded p.
 //
-// Two CTAs share an SM (96 KB of shared memory and 256 columns of tensor memory each): while one's
-// softmax warps work, the other's products run.  Warps 0-3 are the softmax, one thread of warp 4 issues
-// every copy and product.  Every wait is bounded.
+// One CTA an SM stays for the whole call and walks its units as one stream.  Warps 0-3 and 4-7 are the
+// softmax of either tile, warp 8 copies, warp 9 issues the products, in the order
+//     P0(j) ready: P0 V (j), S0(j+1) | P1(j) ready: P1 V (j), S1(j+1) | ...
+// so the tensor pipe works on one tile while the other's softmax runs.  What bounds: an S product alone reads
+// shared memory at its full 128 bytes a cycle, and the copies write there too; two tiles that share each
+// copy of K and V keep that at 2048 cycles a pair of items, the products' own time.  The exponentials
+// take as long: 16 a cycle and SM.  Every wait is bounded.
 #include "attn_tc.cuh"
 #include "launch.h"
 #include "tma_host.h"
@@ -21,58 +27,96 @@ namespace gdn {
 namespace attn {
 namespace {
 
-constexpr int kThreads = 160;
-enum FwdBar { B_K = 0, B_V, B_S, B_P, B_O, B_COUNT };
+constexpr int kThreads = 384;
+constexpr int kCopyWarp = 8, kMmaWarp = 9;  // warps 10 and 11 complete their warpgroup
+// Registers a thread: the launch's, and what the softmax warpgroups and the third take of them
+constexpr int kRegs = 168, kSoftmaxRegs = 200, kOtherRegs = 88;
+static_assert(256 * kSoftmaxRegs + 128 * kOtherRegs <= kThreads * kRegs, "the split waits forever above the launch's total");
 
 template <int D>
 struct FwdSmem {
+    static constexpr int kStages = D == 128 ? 5 : 10;  // ring of K and V tiles, K(0) V(0) K(1) V(1) ..
     static constexpr uint32_t kTile = kRows * D * 2;
-    static constexpr uint32_t kQ = 0, kK = kTile, kV = 2 * kTile, kBar = 3 * kTile;
-    static constexpr uint32_t kBytes = kBar + 128 + 1024;  // + alignment slack
+    static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBar = kRing + kStages * kTile;
+    static constexpr uint32_t kBytes = kBar + 320;  // the dynamic array starts on 1024 bytes
+    static __device__ __forceinline__ uint32_t ring(int i) { return kRing + (uint32_t)(i % kStages) * kTile; }
 };
-constexpr uint32_t TM_S = 0, TM_O = 128, TM_COLS = 256;
+static_assert(FwdSmem<128>::kBytes <= 232448, "227 KB");
+enum FwdBar {
+    B_Q = 0, B_Q_FREE,
+    B_S,                  // [2 tiles] S done
+    B_P = B_S + 2,        // [2] P written (128 threads)
+    B_O = B_P + 2,        // [2] P V done
+    B_R = B_O + 2,        // [stages] landed
+    B_R_FREE = B_R + 10,  // [stages] read for the last time
+    B_COUNT = B_R_FREE + 10
+};
+static_assert(B_COUNT * 8 <= 304, "barriers");
+// tensor memory: S of either tile, O of either tile
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
 struct FwdParams {
     AttnIO io;
-    int tiles;         // bound on the row tiles
+    int tiles;         // bound on the 128-row tiles
     int window;        // INT_MAX: none
     float scale_log2;
 };
 
-template <int D, bool SAVE>
-__global__ void __launch_bounds__(kThreads, 2)
+// The two tiles of a unit: first row within the sequence, query head, and key tiles hi down to lo (hi < lo: the
+// tile does not exist).
+struct Pair {
+    int row0[2], head[2], hi[2], lo[2];
+    int top, bottom;  // key tiles of either
+};
+template <bool PAIR_HEADS>
+__device__ __forceinline__ Pair pair_of(const Seq& sq, int unit_head, int window) {
+    Pair pr;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        pr.row0[s] = PAIR_HEADS ? sq.local * kRows : (2 * sq.local + s) * kRows;
+        pr.head[s] = PAIR_HEADS ? 2 * unit_head + s : unit_head;
+        pr.hi[s] = pr.row0[s] / kRows;
+        pr.lo[s] = pr.row0[s] < sq.len ? max(0, pr.row0[s] - window + 1) / kRows : pr.hi[s] + 1;
+    }
+    const bool two = pr.hi[1] >= pr.lo[1];
+    pr.top = two ? pr.hi[1] : pr.hi[0];
+    pr.bottom = pr.lo[0];  // the first tile exists, and sees at least as far back
+    return pr;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+template <int D, bool SAVE, bool PAIR_HEADS>
+__global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
     using L = FwdSmem<D>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int NS = L::kStages;
+    extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int head = blockIdx.x % p.io.Hq;
-    Seq sq;
-    TileMap map(p.io.cu, p.io.nseq, p.io.T);
-    if (!map.find((int)(blockIdx.x / p.io.Hq), true, sq)) return;
-    const int hk = head / (p.io.Hq / p.io.Hk);
-    const int row0 = sq.local * kRows;  // first row, within the sequence
-    const int first_key = max(0, row0 - p.window + 1);
-    const int hi = sq.local, lo = first_key / kRows, n = hi - lo + 1;
+    const int G = p.io.Hq / p.io.Hk, heads = PAIR_HEADS ? p.io.Hq / 2 : p.io.Hq;
 
     Ctx cx;
     cx.bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBar + 64);
-    cx.abort_flag = reinterpret_cast<volatile int*>(sm + L::kBar + 68);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBar + 304);
+    cx.abort_flag = reinterpret_cast<volatile int*>(sm + L::kBar + 308);
     cx.err = p.io.err;
     cx.wait_ns = p.io.wait_ns ? p.io.wait_ns : kWaitNs;
+    if (sb & 1023u) {
+        if (tid == 0) atomicOr(cx.err, 1);
+        return;
+    }
     if (tid == 0) {
-        mbar_init(cx.bars + B_K, 1);
-        mbar_init(cx.bars + B_V, 1);
-        mbar_init(cx.bars + B_S, 1);
-        mbar_init(cx.bars + B_P, 128);
-        mbar_init(cx.bars + B_O, 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i == B_P || i == B_P + 1 ? 128 : 1);
         *cx.abort_flag = 0;
         mbar_fence_init();
     }
-    if (warp == 4) {
+    if (warp == kMmaWarp) {
         tmem_alloc(tmem_slot, TM_COLS);
         tmem_relinquish();
     }
@@ -80,140 +124,210 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
+    TileMap<PAIR_HEADS ? kRows : 2 * kRows> map(p.io.cu, p.io.nseq, p.io.T);
+    Seq sq;
+    int uh;
+    bool ok = true;
 
-    if (warp == 4) {
-        if ((tid & 31) == 0) {
-            int k_issued = 0, v_issued = 0, k_seen = 0, v_seen = 0;
-            auto load_k = [&](int i) {
-                mbar_arrive_expect_tx(cx.bars + B_K, i == 0 ? 2 * L::kTile : L::kTile);
-                if (i == 0) load_tile<D>(sb + L::kQ, &tm_q, cx.bars + B_K, head, sq.begin + row0);
-                load_tile<D>(sb + L::kK, &tm_k, cx.bars + B_K, hk, sq.begin + (hi - i) * kRows);
-                ++k_issued;
-            };
-            auto load_v = [&](int i) {
-                mbar_arrive_expect_tx(cx.bars + B_V, L::kTile);
-                load_tile<D>(sb + L::kV, &tm_v, cx.bars + B_V, hk, sq.begin + (hi - i) * kRows);
-                ++v_issued;
-            };
-            load_k(0);
-            load_v(0);
-            bool ok = wait_bar(cx, B_K, 0);
-            if (ok) {
-                ++k_seen;
-                mma_ss_rows<D>(tbase + TM_S, sb + L::kQ, sb + L::kK);
-                mma_commit(cx.bars + B_S);
-            }
-            for (int i = 0; ok && i < n; ++i) {
-                if (!(ok = wait_bar(cx, B_S, i & 1))) break;  // S(i) done: the K tile is free
-                if (i + 1 < n) load_k(i + 1);
-                if (!(ok = wait_bar(cx, B_V, i & 1))) break;
-                ++v_seen;
-                if (!(ok = wait_bar(cx, B_P, i & 1))) break;
-                tc_fence_after();
-                mma_ts_rows<D>(tbase + TM_O, tbase + TM_S, sb + L::kV, i > 0);
-                mma_commit(cx.bars + B_O);
-                if (i + 1 == n) break;
-                if (!(ok = wait_bar(cx, B_K, (i + 1) & 1))) break;
-                ++k_seen;
-                // runs after P V (products run in issue order), so it may write over P
-                mma_ss_rows<D>(tbase + TM_S, sb + L::kQ, sb + L::kK);
-                mma_commit(cx.bars + B_S);
-                if (!(ok = wait_bar(cx, B_O, i & 1))) break;  // the V tile is free
-                load_v(i + 1);
-            }
-            // after an expired wait: the copies still on their way land before the memory is given up
-            if (k_seen < k_issued) mbar_wait(cx.bars + B_K, (k_issued - 1) & 1, cx.wait_ns);
-            if (v_seen < v_issued) mbar_wait(cx.bars + B_V, (v_issued - 1) & 1, cx.wait_ns);
-        }
-        __syncwarp();
-    } else {
-        const uint32_t tl = tbase + ((uint32_t)(warp * 32) << 16);
-        const int row = row0 + tid;  // within the sequence
-        float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        for (int i = 0; i < n; ++i) {
-            if (!(ok = wait_warp(cx, B_S, i & 1))) break;
-            // P V of the tile before finished earlier (S was issued after it): its phase is seen here, so
-            // that this thread is never two phases behind
-            if (i && !(ok = wait_warp(cx, B_O, (i - 1) & 1))) break;
-            tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32(tl + TM_S + 32 * c, s[c]);
-            tmem_ld_wait();
-            const int key0 = (hi - i) * kRows;
-            // keys after the row, or out of its window, leave the softmax
-            if (i == 0 || key0 <= row0 + kRows - 1 - p.window) {
-                const int last = row - key0, gone = last - p.window;
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int j = 32 * c + e;
-                        if (j > last || j <= gone) s[c][e] = 0xFF800000u;  // -inf
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kCopyWarp) {
+            int units = 0, ri = 0;  // Q loads and ring loads issued
+            for (int k = 0; ok; ++k) {
+                const int f = map.unit(k, heads, true, sq, uh);
+                if (f == 2) break;
+                if (f == 1) continue;
+                const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
+                const int hk = pr.head[0] / G;
+                if ((tid & 31) == 0) {
+                    auto load = [&](const CUtensorMap* map_, int kt) -> bool {
+                        if (ri >= NS && !wait_bar(cx, B_R_FREE + ri % NS, (ri / NS - 1) & 1)) return false;
+                        uint64_t* bar = cx.bars + B_R + ri % NS;
+                        mbar_arrive_expect_tx(bar, L::kTile);
+                        load_tile<D>(sb + L::ring(ri), map_, bar, hk, sq.begin + kt * kRows);
+                        ++ri;
+                        return true;
+                    };
+                    ok = load(&tm_k, pr.top);  // need not wait for the unit before
+                    if (ok && units) ok = wait_bar(cx, B_Q_FREE, (units - 1) & 1);
+                    if (ok) {
+                        const bool two = pr.hi[1] >= pr.lo[1];
+                        mbar_arrive_expect_tx(cx.bars + B_Q, two ? 2 * L::kTile : L::kTile);
+                        load_tile<D>(sb + L::kQ, &tm_q, cx.bars + B_Q, pr.head[0], sq.begin + pr.row0[0]);
+                        if (two) load_tile<D>(sb + L::kQ + L::kTile, &tm_q, cx.bars + B_Q, pr.head[1], sq.begin + pr.row0[1]);
+                        ++units;
                     }
+                    ok = ok && load(&tm_v, pr.top);
+                    for (int kt = pr.top - 1; ok && kt >= pr.bottom; --kt) ok = load(&tm_k, kt) && load(&tm_v, kt);
+                }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
-            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int e = 0; e < 32; e += 2)
-                    x[c] = fmaxf(x[c], fmaxf(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])));
-            const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
-            if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                const float mn = fmaxf(m, mx), f = i ? exp2_approx(m - mn) : 0.f;
-                m = mn;
-                l *= f;
-                if (i) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(tl + TM_O + 32 * c, o);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t w[16];
-#pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                w[e] = __float_as_uint(__uint_as_float(o[16 * h + e]) * f);
-                            tmem_st16(tl + TM_O + 32 * c + 16 * h, w);
+            if ((tid & 31) == 0 && *cx.abort_flag) {
+                // after an expired wait: the copies still on their way land before the memory is given up
+                if (units) mbar_wait(cx.bars + B_Q, (units - 1) & 1, cx.wait_ns);
+                for (int i = ri < NS ? 0 : ri - NS; i < ri; ++i) mbar_wait(cx.bars + B_R + i % NS, (i / NS) & 1, cx.wait_ns);
+            }
+            __syncwarp();
+        } else if (warp == kMmaWarp) {
+            int units = 0, ri = 0, done[2] = {0, 0};  // Q tiles and ring tiles so far; items of either tile
+            for (int k = 0; ok; ++k) {
+                const int f = map.unit(k, heads, true, sq, uh);
+                if (f == 2) break;
+                if (f == 1) continue;
+                const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
+                if ((tid & 31) == 0) {
+                    auto landed = [&](int i) { return wait_bar(cx, B_R + i % NS, (i / NS) & 1); };
+                    auto sees = [&](int s, int kt) { return kt <= pr.hi[s] && kt >= pr.lo[s]; };
+                    // S of tile s against the K tile in ring slot i
+                    auto s_product = [&](int s, int i) {
+                        mma_ss_rows<D>(tbase + TM_S + 128 * s, sb + L::kQ + (uint32_t)s * L::kTile, sb + L::ring(i));
+                        mma_commit(cx.bars + B_S + s);
+                    };
+                    ok = wait_bar(cx, B_Q, units & 1) && landed(ri);
+                    ++units;
+                    if (ok) {
+                        for (int s = 0; s < 2; ++s)
+                            if (sees(s, pr.top)) s_product(s, ri);
+                        mma_commit(cx.bars + B_R_FREE + ri % NS);
+                        if (pr.top == pr.bottom) mma_commit(cx.bars + B_Q_FREE);
+                    }
+                    // key tile kt: V in slot ri + 1, the next K in ri + 2
+                    for (int kt = pr.top; ok && kt >= pr.bottom; --kt, ri += 2) {
+                        if (!(ok = landed(ri + 1))) break;
+                        const bool more = kt > pr.bottom;
+                        bool next_k = false;
+                        for (int s = 0; s < 2; ++s) {
+                            if (sees(s, kt)) {
+                                if (!(ok = wait_bar(cx, B_P + s, done[s] & 1))) break;
+                                tc_fence_after();
+                                mma_ts_rows<D>(tbase + TM_O + 128 * s, tbase + TM_S + 128 * s, sb + L::ring(ri + 1), kt < pr.hi[s]);
+                                mma_commit(cx.bars + B_O + s);
+                                ++done[s];
+                            }
+                            if (more && sees(s, kt - 1)) {
+                                if (!next_k && !(ok = landed(ri + 2))) break;
+                                next_k = true;
+                                s_product(s, ri + 2);  // runs after P V, so it may write over P
+                            }
+                        }
+                        if (!ok) break;
+                        mma_commit(cx.bars + B_R_FREE + (ri + 1) % NS);
+                        if (more) {
+                            mma_commit(cx.bars + B_R_FREE + (ri + 2) % NS);
+                            if (kt - 1 == pr.bottom) mma_commit(cx.bars + B_Q_FREE);
                         }
                     }
                 }
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
             }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float a = exp2_approx(fmaf(__uint_as_float(s[c][2 * e]), p.scale_log2, -m));
-                    const float b = exp2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), p.scale_log2, -m));
-                    sum[e & 3] += a + b;
-                    w[e] = pack_bf16x2(a, b);
-                }
-                tmem_st16(tl + TM_S + 16 * c, w);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            if (i == 0 && sq.len - key0 < kRows) {
-                // V's rows past the sequence: p is 0 there, but 0 * NaN is not
-                if (!(ok = wait_warp(cx, B_V, 0))) break;
-                if (tid >= sq.len - key0) zero_row<D>(sm + L::kV, tid);
-                fence_async_shared();
-            }
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive(cx.bars + B_P);
+            __syncwarp();
         }
-        if (ok && wait_warp(cx, B_O, (n - 1) & 1)) {
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
+        const int s_ = warp >> 2, lane = tid & 127;  // tile of the pair, row within it
+        const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t t_s = tl + TM_S + 128 * s_, t_o = tl + TM_O + 128 * s_;
+        const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
+        int gi = 0;   // items of this tile so far
+        int ri = 0;   // ring tiles so far
+        for (int k = 0; ok; ++k) {
+            const int f = map.unit(k, heads, true, sq, uh);
+            if (f == 2) break;
+            if (f == 1) continue;
+            const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
+            const int row0 = pr.row0[s_], hi = pr.hi[s_], lo = pr.lo[s_];
+            const int row = row0 + lane;
+            float m = -INFINITY, l = 0.f;
+            for (int kt = hi; kt >= lo; --kt, ++gi) {
+                if (!(ok = wait_warp(cx, B_S + s_, gi & 1))) break;
+                // P V of the tile before finished earlier (S was issued after it): its phase is seen here, so
+                // that this thread is never two phases behind
+                if (kt < hi && !(ok = wait_warp(cx, B_O + s_, (gi - 1) & 1))) break;
+                tc_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s[c]);
+                tmem_ld_wait();
+                const int key0 = kt * kRows;
+                // keys after the row, or out of its window, leave the softmax
+                if (kt == hi || key0 <= row0 + kRows - 1 - p.window) {
+                    const int last = row - key0, gone = last - p.window;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int j = 32 * c + e;
+                            if (j > last || j <= gone) s[c][e] = 0xFF800000u;  // -inf
+                        }
+                }
+                float x[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    x[c] = fmaxf(__uint_as_float(s[c][0]), __uint_as_float(s[c][1]));
+#pragma unroll
+                    for (int e = 2; e < 32; e += 2) x[c] = max3(x[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+                }
+                const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
+                if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                    const float mn = fmaxf(m, mx), f = kt < hi ? exp2_approx(m - mn) : 0.f;
+                    m = mn;
+                    l *= f;
+                    if (kt < hi) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(t_o + 16 * c, o);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(t_o + 16 * c, o);
+                        }
+                    }
+                }
+                const f2 nm = f2_of(-m, -m);
+                f2 sum[2] = {f2_of(0.f, 0.f), f2_of(0.f, 0.f)};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float a, b;
+                        f2_get(f2_fma(f2_of(s[c][2 * e], s[c][2 * e + 1]), scale2, nm), a, b);
+                        a = exp2_approx(a);
+                        b = exp2_approx(b);
+                        sum[e & 1] = f2_add(sum[e & 1], f2_of(a, b));
+                        w[e] = pack_bf16x2(a, b);
+                    }
+                    tmem_st16(t_s + 16 * c, w);
+                }
+                float a, b;
+                f2_get(f2_add(sum[0], sum[1]), a, b);
+                l += a + b;
+                if (kt == hi && sq.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
+                    // V's rows past the sequence: p is 0 there, but 0 * NaN is not.  Two heads share the tile,
+                    // whose product with P1 follows the one with P0.
+                    const int slot = ri + 2 * (pr.top - kt) + 1;
+                    if (!(ok = wait_warp(cx, B_R + slot % NS, (slot / NS) & 1))) break;
+                    if (lane >= sq.len - key0) zero_row<D>(sm + L::ring(slot), lane);
+                    fence_async_shared();
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive(cx.bars + B_P + s_);
+            }
+            ri += 2 * (pr.top - pr.bottom + 1);
+            if (!ok) break;
+            if (hi < lo) continue;
+            if (!(ok = wait_warp(cx, B_O + s_, (gi - 1) & 1))) break;
             tc_fence_after();
+            // the next unit's first product into O waits for its P, which follows this
             const bool live = row < sq.len;
             const float inv = 1.f / l;
-            const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + head) * D;
+            const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + pr.head[s_]) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
-                tmem_ld32(tl + TM_O + 32 * c, o);
+                tmem_ld32(t_o + 32 * c, o);
                 tmem_ld_wait();
                 float v[32];
 #pragma unroll
@@ -228,24 +342,35 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
             }
             // every row of the tile, so that the backward's copies of it read no uninitialised memory
-            if (SAVE) p.io.lse[((int64_t)head * p.tiles + sq.tile) * kRows + tid] = live ? -(m + log2f(l)) : 0.f;
+            if (SAVE) {
+                const int tile = sq.tile + (PAIR_HEADS ? 0 : s_);
+                p.io.lse[((int64_t)pr.head[s_] * p.tiles + tile) * kRows + lane] = live ? -(m + log2f(l)) : 0.f;
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 4) tmem_dealloc(tbase, TM_COLS);
+    if (warp == kMmaWarp) tmem_dealloc(tbase, TM_COLS);
 }
 
-template <int D, bool SAVE>
+template <int D, bool SAVE, bool PAIR_HEADS>
 cudaError_t launch(const CUtensorMap* maps, const FwdParams& p, cudaStream_t st) {
-    auto kernel = attn_fwd_kernel<D, SAVE>;
+    auto kernel = attn_fwd_kernel<D, SAVE, PAIR_HEADS>;
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdSmem<D>::kBytes);
+    cudaFuncAttributes attr;
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)p.tiles * (unsigned)p.io.Hq, kThreads, FwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], p);
+    if (attr.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // setmaxnreg counts on them
+    const int64_t units = (int64_t)p.tiles * p.io.Hq / (PAIR_HEADS ? 2 : 1);
+    kernel<<<(unsigned)(units < 148 ? units : 148), kThreads, FwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], p);
     count_launch();
     return cudaGetLastError();
+}
+template <int D, bool SAVE>
+cudaError_t launch_s(const CUtensorMap* maps, const FwdParams& p, cudaStream_t st) {
+    return p.io.Hq / p.io.Hk % 2 == 0 ? launch<D, SAVE, true>(maps, p, st) : launch<D, SAVE, false>(maps, p, st);
 }
 
 }  // namespace
@@ -262,8 +387,8 @@ cudaError_t attn_fwd(const AttnIO& io, int d, cudaStream_t st) {
     p.tiles = (int)attn_tiles(io.T, io.nseq);
     p.window = io.window > 0 && io.window < INT32_MAX ? (int)io.window : INT32_MAX;
     p.scale_log2 = io.scale * 1.4426950408889634f;
-    if (d == 128) return io.lse ? attn::launch<128, true>(maps, p, st) : attn::launch<128, false>(maps, p, st);
-    return io.lse ? attn::launch<64, true>(maps, p, st) : attn::launch<64, false>(maps, p, st);
+    if (d == 128) return io.lse ? attn::launch_s<128, true>(maps, p, st) : attn::launch_s<128, false>(maps, p, st);
+    return io.lse ? attn::launch_s<64, true>(maps, p, st) : attn::launch_s<64, false>(maps, p, st);
 }
 
 }  // namespace gdn

@@ -27,49 +27,62 @@ constexpr int kRows = 128;
 
 struct Seq {
     int begin, len;   // first token, tokens
-    int tile, local;  // global tile number, tile within the sequence
+    int tile, local;  // global number of its (first) 128-row tile, tile within the sequence
 };
 
-// The map from a CTA's units of work to tiles, one per warp (every call is warp-collective).  With up to 32
-// sequences the tiles come in descending order of their work: a tile of a causal sequence of t tiles has
-// 1, 2, .. or t tiles to look at, one tile of each (a window caps the larger ones, which keeps the order), so
-// the r-th heaviest is found by counting.  With more sequences they come in the sequences' order.
+// The map from a CTA's units of work to tiles of R rows (128 or 256), one per warp (every call is
+// warp-collective).  With up to 32 sequences the tiles come in descending order of their work: a tile of a
+// causal sequence of t tiles has 1, 2, .. or t tiles to look at, one tile of each (a window caps the larger
+// ones, which keeps the order), so the r-th heaviest is found by counting.  With more sequences they come in the
+// sequences' order.
+template <int R>
 struct TileMap {
     const int32_t* cu;
     int nseq, T;
-    int b, e, t, first;  // up to 32 sequences: this lane's one, its tiles and the first of them
+    int b, e, t;         // up to 32 sequences: this lane's one, its tiles,
+    int first, first128;  // and the tiles before them, of R and of 128 rows
     int total;           // tiles
 
-    __device__ __forceinline__ void bounds(int s, int& x, int& y) const {
-        x = y = 0;
-        if (s < nseq) {
-            x = min(max(__ldg(cu + s), 0), T);
-            y = min(max(__ldg(cu + s + 1), x), T);
-        }
-    }
     static __device__ __forceinline__ int scan(int x) {  // inclusive
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if ((threadIdx.x & 31) >= o) x += y;
+            if ((int)(threadIdx.x & 31) >= o) x += y;
         }
         return x;
     }
-    __device__ __forceinline__ TileMap(const int32_t* cu_, int nseq_, int T_) : cu(cu_), nseq(nseq_), T(T_) {
-        total = 0;
-        for (int s0 = 0; s0 < nseq; s0 += 32) {
-            bounds(s0 + (threadIdx.x & 31), b, e);
-            t = (e - b + kRows - 1) / kRows;
-            const int incl = scan(t);
-            first = incl - t;
-            total += __shfl_sync(0xffffffffu, incl, 31);
+    // The 32 sequences from s0 on, `before` and `before128` tiles into the batch.
+    __device__ __forceinline__ void load(int s0, int& before, int& before128) {
+        const int s = s0 + (int)(threadIdx.x & 31);
+        b = e = 0;
+        if (s < nseq) {
+            b = min(max(__ldg(cu + s), 0), T);
+            e = min(max(__ldg(cu + s + 1), b), T);
         }
+        t = (e - b + R - 1) / R;
+        int incl = scan(t);
+        first = before + incl - t;
+        before += __shfl_sync(0xffffffffu, incl, 31);
+        if (R == kRows) {
+            first128 = first;
+            before128 = before;
+        } else {
+            const int t128 = (e - b + kRows - 1) / kRows;
+            incl = scan(t128);
+            first128 = before128 + incl - t128;
+            before128 += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    __device__ __forceinline__ TileMap(const int32_t* cu_, int nseq_, int T_) : cu(cu_), nseq(nseq_), T(T_) {
+        int before = 0, before128 = 0;
+        for (int s0 = 0; s0 < nseq; s0 += 32) load(s0, before, before128);
+        total = before;
     }
     __device__ __forceinline__ void take(Seq& out, int src, int local) const {
         out.begin = __shfl_sync(0xffffffffu, b, src);
         out.len = __shfl_sync(0xffffffffu, e, src) - out.begin;
         out.local = local;
-        out.tile = __shfl_sync(0xffffffffu, first, src) + local;
+        out.tile = __shfl_sync(0xffffffffu, first128, src) + local * (R / kRows);
     }
     // Tile `rank` of the order; up: the work grows with the tile's place in its sequence (query tiles, which
     // see the keys before them), else it falls (key tiles).  False past the last one.
@@ -93,19 +106,15 @@ struct TileMap {
             return true;
         }
         const int g = up ? total - 1 - rank : rank;
-        int before = 0;
+        int before = 0, before128 = 0;
         for (int s0 = 0;; s0 += 32) {
-            bounds(s0 + lane, b, e);
-            t = (e - b + kRows - 1) / kRows;
-            const int incl = scan(t);
-            first = before + incl - t;
+            load(s0, before, before128);
             const uint32_t hit = __ballot_sync(0xffffffffu, g >= first && g < first + t);
             if (hit) {
                 const int src = __ffs(hit) - 1;
                 take(out, src, g - __shfl_sync(0xffffffffu, first, src));
                 return true;
             }
-            before += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
     // Unit k of this CTA's share of `heads` times the tiles: rows of the grid's width in the order above,
