@@ -43,23 +43,25 @@ struct BwdSmem {
     static constexpr uint32_t kA = 2 * kTile, kB = 5 * kTile;  // [3] and [2] stages
     static constexpr uint32_t kStats = 7 * kTile;              // dkdv: [2][-lse, -delta][128]
     static constexpr uint32_t kBar = kStats + 2 * 1024;
-    static constexpr uint32_t kBytes = kBar + 160;             // the dynamic array starts on 1024 bytes
+    static constexpr uint32_t kBytes = kBar + 176;             // the dynamic array starts on 1024 bytes
     static __device__ __forceinline__ uint32_t a(int i) { return kA + (uint32_t)(i % 3) * kTile; }
     static __device__ __forceinline__ uint32_t b(int i) { return kB + (uint32_t)(i & 1) * kTile; }
 };
 static_assert(BwdSmem<128>::kBytes <= 232448, "227 KB");
-constexpr uint32_t TM_S = 0, TM_DP = 128, TM_ACC0 = 256, TM_ACC1 = 384, TM_COLS = 512;
+constexpr uint32_t TM_S = 0, TM_DP = 128, TM_ACC0 = 256, TM_ACC1 = 384, TM_DS = 384, TM_COLS = 512;
+constexpr int kPoly = 2;  // of 8 exponentials on the FMA pipe
 
 enum BwdBar {
     B_OWN = 0, B_OWN_FREE,      // own tiles landed; read for the last time
-    B_A, B_A_FREE = B_A + 3,    // stages of A
-    B_B = B_A_FREE + 3, B_B_FREE = B_B + 2,
-    B_S = B_B_FREE + 2, B_DP,   // products done
-    B_X, B_DS,                  // element-wise steps done (every thread arrives)
+    B_A, B_B = B_A + 3,         // stages of A and B landed
+    B_FREE = B_B + 2,           // [4] item's stages (dq: A's) read for the last time (item mod 4)
+    B_V_FREE = B_FREE + 4,      // [2] dq: stages of B read for the last time
+    B_S = B_V_FREE + 2, B_DP,   // products done
+    B_X, B_Y, B_DS,             // element-wise steps done (an arrival a warp)
     B_END,                      // the unit's accumulators are complete
     B_COUNT
 };
-static_assert(B_COUNT * 8 <= 144, "barriers");
+static_assert(B_COUNT * 8 <= 160, "barriers");
 
 struct BwdParams {
     AttnIO io;
@@ -70,8 +72,8 @@ struct BwdParams {
 // Barriers, tensor memory; false if the shared array does not start where the tiles need it.
 __device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const AttnIO& io, uint32_t*& tmem_slot) {
     cx.bars = reinterpret_cast<uint64_t*>(bars);
-    tmem_slot = reinterpret_cast<uint32_t*>(bars + 144);
-    cx.abort_flag = reinterpret_cast<volatile int*>(bars + 148);
+    tmem_slot = reinterpret_cast<uint32_t*>(bars + 160);
+    cx.abort_flag = reinterpret_cast<volatile int*>(bars + 164);
     cx.err = io.err;
     cx.wait_ns = io.wait_ns ? io.wait_ns : kWaitNs;
     if (smem_u32(sm) & 1023u) {
@@ -79,7 +81,7 @@ __device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const
         return false;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i == B_X || i == B_DS ? kElem : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i >= B_X && i <= B_DS ? kElem / 32 : 1);
         *cx.abort_flag = 0;
         mbar_fence_init();
     }
@@ -105,41 +107,50 @@ __device__ __forceinline__ void drain(const Ctx& cx, int owns, int a_items, int 
 }
 
 // D (+)= A B with A [128 x 128] bf16 in tensor memory as two halves of 32 columns, 64 columns apart, and
-// B a row tile taken MN-major.
-template <int D>
-__device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem, bool accumulate) {
+// B a row tile taken MN-major; of either half the quarters Q0 .. Q1 - 1 (16 of its 64 rows of B each).
+template <int D, int Q0, int Q1>
+__device__ __forceinline__ void mma_halves(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_desc, bool accumulate) {
     constexpr uint32_t idesc = idesc_bf16_f32_mn(128, D, false, true);
-    const uint64_t db = sdesc_mn_sw128(b_smem, kRows * 128u);
 #pragma unroll
-    for (int k = 0; k < kRows; k += 16)
-        mma_ts(d_tmem, a_tmem + (uint32_t)((k >> 6) * 64 + ((k & 63) >> 1)), db + (uint64_t)((k * 128) >> 4), idesc,
-               (accumulate || k > 0) ? 1u : 0u);
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = Q0; q < Q1; ++q)
+            mma_ts(d_tmem, a_tmem + (uint32_t)(h * 64 + q * 8), desc_of(b_desc + (uint32_t)(((h * 64 + q * 16) * 128) >> 4)),
+                   idesc, (accumulate || h > 0 || q > Q0) ? 1u : 0u);
 }
 
-// 64 floats as bf16 pairs into 32 columns.
-__device__ __forceinline__ void st_half(uint32_t taddr, const f2 (&x)[32]) {
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            float lo, hi;
-            f2_get(x[16 * q + e], lo, hi);
-            w[e] = pack_bf16x2(lo, hi);
+// The issuing thread's place in the stream of items: stages of A and B, and the phase bits of the barriers.
+template <int D>
+struct ItemAt {
+    static constexpr uint32_t kStep = BwdSmem<D>::kTile >> 4;
+    uint32_t a = 0, a_phase = 0, b = 0, b_phase = 0, phase = 0, mod4 = 0;
+    __device__ __forceinline__ void next() {
+        if (++a == 3) {
+            a = 0;
+            a_phase ^= 1u;
         }
-        tmem_st16(taddr + 16 * q, w);
+        b ^= 1u;
+        b_phase ^= b ^ 1u;  // flips when b returns to 0
+        phase ^= 1u;
+        mod4 = (mod4 + 1) & 3;
     }
-}
-// p = exp2(s c + nl) for a pair.
-__device__ __forceinline__ f2 exp_pair(uint32_t s0, uint32_t s1, f2 c, f2 nl) {
-    float a, b;
-    f2_get(f2_fma(f2_of(s0, s1), c, nl), a, b);
-    return f2_of(exp2_approx(a), exp2_approx(b));
+};
+
+// 32 floats (16 pairs) as bf16 pairs into 16 columns.
+__device__ __forceinline__ void st_quarter(uint32_t taddr, const f2* x) {
+    uint32_t w[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+        float lo, hi;
+        f2_get(x[e], lo, hi);
+        w[e] = pack_bf16x2(lo, hi);
+    }
+    tmem_st16(taddr, w);
 }
 // Columns outside [lo, hi] to 0.
-__device__ __forceinline__ void mask_pairs(f2 (&x)[32], int lo, int hi) {
+__device__ __forceinline__ void mask_pairs(f2* x, int lo, int hi) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < 16; ++c) {
         float a, b;
         f2_get(x[c], a, b);
         x[c] = f2_of(2 * c < lo || 2 * c > hi ? 0.f : a, 2 * c + 1 < lo || 2 * c + 1 > hi ? 0.f : b);
@@ -182,7 +193,7 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
     TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
-    Seq sq;
+    Seq sq{};
     int hk;
     bool ok = true;
     int gi = 0;  // items so far, over all units: the stages' and barriers' phases go by it
@@ -197,12 +208,12 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if ((tid & 31) == 0) {
                 for (int it = 0; ok && it < m; ++it, ++gi) {
                     const int head = hk * G + it / nq, tile = it % nq;
-                    if (gi >= 3 && !(ok = wait_bar(cx, B_A_FREE + gi % 3, (gi / 3 - 1) & 1))) break;
+                    // A's stage was freed with item gi - 3, which the load before this one has waited for
                     uint64_t* bar = cx.bars + B_A + gi % 3;
                     mbar_arrive_expect_tx(bar, L::kTile);
                     load_tile<D>(sb + L::a(gi), &tm_q, bar, head, key0 + tile * kRows);
                     ++a_items;
-                    if (gi >= 2 && !(ok = wait_bar(cx, B_B_FREE + (gi & 1), ((gi >> 1) - 1) & 1))) break;
+                    if (gi >= 2 && !(ok = wait_bar(cx, B_FREE + ((gi - 2) & 3), ((gi - 2) >> 2) & 1))) break;
                     bar = cx.bars + B_B + (gi & 1);
                     mbar_arrive_expect_tx(bar, L::kTile + 2 * kRows * 4);
                     load_tile<D>(sb + L::b(gi), &tm_do, bar, head, key0 + tile * kRows);
@@ -224,44 +235,49 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if ((tid & 31) == 0) drain(cx, owns, a_items, b_items);
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        int owns = 0;
+        using At = ItemAt<D>;
+        At at, nx;  // the item, and the one after it
+        nx.next();
+        uint32_t own_phase = 0;
+        const uint32_t own0 = desc_k(sb + L::kOwn0), own1 = desc_k(sb + L::kOwn1);
+        const uint32_t ak = desc_k(sb + L::kA), bk = desc_k(sb + L::kB), am = desc_mn(sb + L::kA), bm = desc_mn(sb + L::kB);
         for (int k = 0; ok; ++k) {
             const int f = map.unit(k, p.io.Hk, false, sq, hk);
             if (f == 2) break;
             if (f == 1) continue;
             const int m = G * query_tiles(sq, p.window);
             if ((tid & 31) == 0) {
-                auto s_product = [&](int i) {
-                    mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::a(i));
+                auto s_product = [&](const At& i) -> bool {
+                    if (!wait_bar(cx, B_A + i.a, i.a_phase)) return false;
+                    mma_ss_rows<D>(tbase + TM_S, own0, ak + i.a * At::kStep);
                     mma_commit(cx.bars + B_S);
+                    return true;
                 };
-                auto dp_product = [&](int i, bool last) {
-                    mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::b(i));
+                auto dp_product = [&](const At& i, bool last) -> bool {
+                    if (!wait_bar(cx, B_B + i.b, i.b_phase)) return false;
+                    mma_ss_rows<D>(tbase + TM_DP, own1, bk + i.b * At::kStep);
                     mma_commit(cx.bars + B_DP);
                     if (last) mma_commit(cx.bars + B_OWN_FREE);
+                    return true;
                 };
-                ok = wait_bar(cx, B_OWN, owns & 1) && wait_bar(cx, B_A + gi % 3, (gi / 3) & 1);
-                ++owns;
-                if (ok) s_product(gi);
-                if (ok && (ok = wait_bar(cx, B_B + (gi & 1), (gi >> 1) & 1))) dp_product(gi, m == 1);
-                for (int it = 0; ok && it < m; ++it, ++gi) {
-                    if (!(ok = wait_bar(cx, B_X, gi & 1))) break;
+                ok = wait_bar(cx, B_OWN, own_phase) && s_product(at) && dp_product(at, m == 1);
+                own_phase ^= 1u;
+                for (int it = 0; ok && it < m; ++it) {
+                    if (!(ok = wait_bar(cx, B_X, at.phase))) break;
                     tc_fence_after();
-                    mma_halves<D>(tbase + TM_ACC0, tbase + TM_S, sb + L::b(gi), it > 0);
-                    if (it + 1 < m) {
-                        if (!(ok = wait_bar(cx, B_A + (gi + 1) % 3, ((gi + 1) / 3) & 1))) break;
-                        s_product(gi + 1);  // runs after dV, so it may write over P
-                    }
-                    if (!(ok = wait_bar(cx, B_DS, gi & 1))) break;
+                    mma_halves<D, 0, 2>(tbase + TM_ACC0, tbase + TM_S, bm + at.b * At::kStep, it > 0);
+                    if (!(ok = wait_bar(cx, B_Y, at.phase))) break;
                     tc_fence_after();
-                    mma_halves<D>(tbase + TM_ACC1, tbase + TM_DP, sb + L::a(gi), it > 0);
-                    mma_commit(cx.bars + B_A_FREE + gi % 3);
-                    mma_commit(cx.bars + B_B_FREE + (gi & 1));
+                    mma_halves<D, 2, 4>(tbase + TM_ACC0, tbase + TM_S, bm + at.b * At::kStep, true);
+                    if (it + 1 < m && !(ok = s_product(nx))) break;  // runs after dV, so it may write over P
+                    if (!(ok = wait_bar(cx, B_DS, at.phase))) break;
+                    tc_fence_after();
+                    mma_halves<D, 0, 4>(tbase + TM_ACC1, tbase + TM_DP, am + at.a * At::kStep, it > 0);
+                    mma_commit(cx.bars + B_FREE + at.mod4);
                     if (it + 1 == m) mma_commit(cx.bars + B_END);
-                    else {
-                        if (!(ok = wait_bar(cx, B_B + ((gi + 1) & 1), ((gi + 1) >> 1) & 1))) break;
-                        dp_product(gi + 1, it + 2 == m);
-                    }
+                    else if (!(ok = dp_product(nx, it + 2 == m))) break;
+                    at = nx;
+                    nx.next();
                 }
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -289,30 +305,33 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_ld32(tl + TM_S + 64 * h, s[0]);
                 tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
                 tmem_ld_wait();
-                f2 x[32];
-#pragma unroll
-                for (int c = 0; c < 32; c += 2) {
-                    const float4 l4 = *reinterpret_cast<const float4*>(nlse + 2 * c);
-                    x[c] = exp_pair(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31], scale2, f2_of(l4.x, l4.y));
-                    x[c + 1] = exp_pair(s[c >> 4][(2 * c + 2) & 31], s[c >> 4][(2 * c + 3) & 31], scale2, f2_of(l4.z, l4.w));
-                }
                 // rows before the key, past its window or past the sequence
                 const bool tail = q0 + kRows > sq.len;
                 const bool masked = tile == 0 || tail || q0 + kRows - 1 - key0 >= p.window;
-                if (masked) {
-                    const int row0 = q0 + 64 * h;
-                    mask_pairs(x, key - row0, min(p.window - 1 < sq.len ? key + p.window - 1 : sq.len - 1, sq.len - 1) - row0);
-                }
-                st_half(tl + TM_S + 64 * h, x);
+                const int row0 = q0 + 64 * h;
+                const int last = min(p.window - 1 < sq.len ? key + p.window - 1 : sq.len - 1, sq.len - 1) - row0;
                 if (tail) {
                     // rows past the sequence have weight 0, but 0 * NaN is not 0; both first products have read them
                     if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
                     if (lane >= sq.len - q0) zero_row<D>(sm + (h ? L::b(gi) : L::a(gi)), lane);
                     fence_async_shared();
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(cx.bars + B_X);
+                f2 x[32];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        const float4 l4 = *reinterpret_cast<const float4*>(nlse + 32 * q + 2 * c);
+                        const f2 a = f2_fma(f2_of(s[q][2 * c], s[q][2 * c + 1]), scale2, f2_of(l4.x, l4.y));
+                        const f2 b = f2_fma(f2_of(s[q][2 * c + 2], s[q][2 * c + 3]), scale2, f2_of(l4.z, l4.w));
+                        x[16 * q + c] = (c & 7) < kPoly ? exp2_pair<true>(a) : exp2_pair<false>(a);
+                        x[16 * q + c + 1] = ((c + 1) & 7) < kPoly ? exp2_pair<true>(b) : exp2_pair<false>(b);
+                    }
+                    if (masked) mask_pairs(x + 16 * q, key - row0 - 32 * q, last - 32 * q);
+                    st_quarter(tl + TM_S + 64 * h + 16 * q, x + 16 * q);
+                    tmem_st_wait();
+                    arrive_warp(cx, q ? B_Y : B_X);
+                }
                 if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
                 tc_fence_after();
                 tmem_ld32(tl + TM_DP + 64 * h, s[0]);
@@ -334,10 +353,10 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     x[c + 1] = f2_mul(x[c + 1],
                                       f2_add(f2_of(s[c >> 4][(2 * c + 2) & 31], s[c >> 4][(2 * c + 3) & 31]), f2_of(d4.z, d4.w)));
                 }
-                st_half(tl + TM_DP + 64 * h, x);
+                st_quarter(tl + TM_DP + 64 * h, x);
+                st_quarter(tl + TM_DP + 64 * h + 16, x + 16);
                 tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(cx.bars + B_DS);
+                arrive_warp(cx, B_DS);
             }
             if (!ok || !(ok = wait_warp(cx, B_END, units & 1))) break;
             ++units;
@@ -368,7 +387,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
     TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
-    Seq sq;
+    Seq sq{};
     int head;
     bool ok = true;
     int gi = 0;
@@ -385,12 +404,12 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if ((tid & 31) == 0) {
                 for (int it = 0; ok && it < m; ++it, ++gi) {
                     const int row = row0 - it * kRows;
-                    if (gi >= 3 && !(ok = wait_bar(cx, B_A_FREE + gi % 3, (gi / 3 - 1) & 1))) break;
+                    if (gi >= 3 && !(ok = wait_bar(cx, B_FREE + ((gi - 3) & 3), ((gi - 3) >> 2) & 1))) break;
                     uint64_t* bar = cx.bars + B_A + gi % 3;
                     mbar_arrive_expect_tx(bar, L::kTile);
                     load_tile<D>(sb + L::a(gi), &tm_k, bar, hk, row);
                     ++a_items;
-                    if (gi >= 2 && !(ok = wait_bar(cx, B_B_FREE + (gi & 1), ((gi >> 1) - 1) & 1))) break;
+                    if (gi >= 2 && !(ok = wait_bar(cx, B_V_FREE + (gi & 1), ((gi >> 1) - 1) & 1))) break;
                     bar = cx.bars + B_B + (gi & 1);
                     mbar_arrive_expect_tx(bar, L::kTile);
                     load_tile<D>(sb + L::b(gi), &tm_v, bar, hk, row);
@@ -409,43 +428,48 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         if ((tid & 31) == 0) drain(cx, owns, a_items, b_items);
         __syncwarp();
     } else if (warp == kMmaWarp) {
-        int owns = 0;
+        using At = ItemAt<D>;
+        At at, nx;  // the item, and the one after it
+        nx.next();
+        uint32_t own_phase = 0;
+        const uint32_t own0 = desc_k(sb + L::kOwn0), own1 = desc_k(sb + L::kOwn1);
+        const uint32_t ak = desc_k(sb + L::kA), bk = desc_k(sb + L::kB), am = desc_mn(sb + L::kA);
         for (int k = 0; ok; ++k) {
             const int f = map.unit(k, p.io.Hq, true, sq, head);
             if (f == 2) break;
             if (f == 1) continue;
             const int m = key_tiles();
             if ((tid & 31) == 0) {
-                auto s_product = [&](int i) {
-                    mma_ss_rows<D>(tbase + TM_S, sb + L::kOwn0, sb + L::a(i));
-                    mma_commit(cx.bars + B_S);
-                };
-                auto dp_product = [&](int i, bool last) {
-                    mma_ss_rows<D>(tbase + TM_DP, sb + L::kOwn1, sb + L::b(i));
-                    mma_commit(cx.bars + B_DP);
-                    mma_commit(cx.bars + B_B_FREE + (i & 1));
-                    if (last) mma_commit(cx.bars + B_OWN_FREE);
-                };
-                ok = wait_bar(cx, B_OWN, owns & 1) && wait_bar(cx, B_A + gi % 3, (gi / 3) & 1);
-                ++owns;
-                if (ok) s_product(gi);
-                if (ok && (ok = wait_bar(cx, B_B + (gi & 1), (gi >> 1) & 1))) dp_product(gi, m == 1);
-                for (int it = 0; ok && it < m; ++it, ++gi) {
-                    if (!(ok = wait_bar(cx, B_X, gi & 1))) break;  // S is in registers
-                    if (it + 1 < m) {
-                        if (!(ok = wait_bar(cx, B_A + (gi + 1) % 3, ((gi + 1) / 3) & 1))) break;
-                        tc_fence_after();
-                        s_product(gi + 1);
-                    }
-                    if (!(ok = wait_bar(cx, B_DS, gi & 1))) break;
+                auto s_product = [&](const At& i) -> bool {
+                    if (!wait_bar(cx, B_A + i.a, i.a_phase)) return false;
                     tc_fence_after();
-                    mma_halves<D>(tbase + TM_ACC0, tbase + TM_DP, sb + L::a(gi), it > 0);
-                    mma_commit(cx.bars + B_A_FREE + gi % 3);
+                    mma_ss_rows<D>(tbase + TM_S, own0, ak + i.a * At::kStep);
+                    mma_commit(cx.bars + B_S);
+                    return true;
+                };
+                auto dp_product = [&](const At& i, bool last) -> bool {
+                    if (!wait_bar(cx, B_B + i.b, i.b_phase)) return false;
+                    tc_fence_after();
+                    mma_ss_rows<D>(tbase + TM_DP, own1, bk + i.b * At::kStep);
+                    mma_commit(cx.bars + B_DP);
+                    mma_commit(cx.bars + B_V_FREE + i.b);
+                    if (last) mma_commit(cx.bars + B_OWN_FREE);
+                    return true;
+                };
+                ok = wait_bar(cx, B_OWN, own_phase) && s_product(at) && dp_product(at, m == 1);
+                own_phase ^= 1u;
+                for (int it = 0; ok && it < m; ++it) {
+                    if (!(ok = wait_bar(cx, B_X, at.phase))) break;  // S is in registers
+                    if (it + 1 < m && !(ok = s_product(nx))) break;
+                    if (!(ok = wait_bar(cx, B_Y, at.phase))) break;  // so is dP
+                    if (it + 1 < m && !(ok = dp_product(nx, it + 2 == m))) break;
+                    if (!(ok = wait_bar(cx, B_DS, at.phase))) break;
+                    tc_fence_after();
+                    mma_ts_rows<D, 0, 128>(tbase + TM_ACC0, tbase + TM_DS, am + at.a * At::kStep, it > 0);
+                    mma_commit(cx.bars + B_FREE + at.mod4);
                     if (it + 1 == m) mma_commit(cx.bars + B_END);
-                    else {
-                        if (!(ok = wait_bar(cx, B_B + ((gi + 1) & 1), ((gi + 1) >> 1) & 1))) break;
-                        dp_product(gi + 1, it + 2 == m);
-                    }
+                    at = nx;
+                    nx.next();
                 }
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
@@ -472,22 +496,26 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tmem_ld32(tl + TM_S + 64 * h, s[0]);
                 tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
                 tmem_ld_wait();
-                tc_fence_before();
-                mbar_arrive(cx.bars + B_X);
+                arrive_warp(cx, B_X);
                 f2 x[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) x[c] = exp_pair(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31], scale2, nlse2);
+                for (int c = 0; c < 32; ++c) {
+                    const f2 y = f2_fma(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), scale2, nlse2);
+                    x[c] = (c & 7) < kPoly ? exp2_pair<true>(y) : exp2_pair<false>(y);
+                }
                 // keys after the row or out of its window
                 const bool masked = it == 0 || key0 <= row0 + kRows - 1 - p.window;
                 if (masked) {
                     const int last = row - key0 - 64 * h;
                     mask_pairs(x, last - p.window + 1, last);
+                    mask_pairs(x + 16, last - p.window + 1 - 32, last - 32);
                 }
                 if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
                 tc_fence_after();
                 tmem_ld32(tl + TM_DP + 64 * h, s[0]);
                 tmem_ld32(tl + TM_DP + 64 * h + 32, s[1]);
                 tmem_ld_wait();
+                arrive_warp(cx, B_Y);
                 if (masked) {  // where the weight is 0, do . v may be anything
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
@@ -500,15 +528,17 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
                     x[c] = f2_mul(x[c], f2_add(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), ndelta2));
-                st_half(tl + TM_DP + 64 * h, x);
+                // dQ of the item before has read its dS
+                if (gi && !(ok = wait_warp(cx, B_FREE + ((gi - 1) & 3), ((gi - 1) >> 2) & 1))) break;
+                st_quarter(tl + TM_DS + 32 * h, x);
+                st_quarter(tl + TM_DS + 32 * h + 16, x + 16);
                 if (it == 0 && sq.len - key0 < kRows) {
-                    // K's rows past the sequence: their ds is 0, but 0 * NaN is not; S and dP are done with them
+                    // K's rows past the sequence: their ds is 0, but 0 * NaN is not; S is done with them
                     if (h == 0 && lane >= sq.len - key0) zero_row<D>(sm + L::a(gi), lane);
                     fence_async_shared();
                 }
                 tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(cx.bars + B_DS);
+                arrive_warp(cx, B_DS);
             }
             if (!ok || !(ok = wait_warp(cx, B_END, units & 1))) break;
             ++units;
@@ -528,7 +558,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int tiles) {
     constexpr int LANES = D / 8, RPP = 256 / LANES;
-    Seq sq;
+    Seq sq{};
     const int head = blockIdx.x % io.Hq;
     TileMap<kRows> map(io.cu, io.nseq, io.T);
     if (!map.find((int)(blockIdx.x / io.Hq), false, sq)) return;

@@ -15,7 +15,10 @@
 // One CTA an SM stays for the whole call and walks its units as one stream.  Warps 0-3 and 4-7 are the
 // softmax of either tile, warp 8 copies, warp 9 issues the products, in the order
 //     P0(j) ready: P0 V (j), S0(j+1) | P1(j) ready: P1 V (j), S1(j+1) | ...
-// so the tensor pipe works on one tile while the other's softmax runs.  What bounds: an S product alone reads
+// so the tensor pipe works on one tile while the other's softmax runs.  (One issuer: two let the tiles' products
+// interleave, which lengthens both chains: 381 us against 300 for 8192 tokens, 16 heads.)  A tile's own chain is
+// its softmax, P V, S, and about 460 cycles until a product's end is seen; P goes over in two halves, so that
+// the first half of P V runs under the second half's exponentials.  What bounds: an S product alone reads
 // shared memory at its full 128 bytes a cycle, and the copies write there too; two tiles that share each
 // copy of K and V keep that at 2048 cycles a pair of items, the products' own time.  The exponentials
 // take as long: 16 a cycle and SM.  Every wait is bounded.
@@ -45,13 +48,15 @@ static_assert(FwdSmem<128>::kBytes <= 232448, "227 KB");
 enum FwdBar {
     B_Q = 0, B_Q_FREE,
     B_S,                  // [2 tiles] S done
-    B_P = B_S + 2,        // [2] P written (128 threads)
-    B_O = B_P + 2,        // [2] P V done
+    B_PA = B_S + 2,       // [2] first half of P written (an arrival a warp)
+    B_PB = B_PA + 2,      // [2] second half
+    B_O = B_PB + 2,       // [2] the unit's last P V done
     B_R = B_O + 2,        // [stages] landed
-    B_R_FREE = B_R + 10,  // [stages] read for the last time
-    B_COUNT = B_R_FREE + 10
+    B_R_FREE = B_R + 10,  // [4] ring tiles 2q + 1 and 2q + 2 read for the last time (q mod 4)
+    B_COUNT = B_R_FREE + 4
 };
 static_assert(B_COUNT * 8 <= 304, "barriers");
+constexpr int kPoly = 3;  // of 8 exponentials on the FMA pipe
 // tensor memory: S of either tile, O of either tile
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
@@ -64,24 +69,74 @@ struct FwdParams {
 
 // The two tiles of a unit: first row within the sequence, query head, and key tiles hi down to lo (hi < lo: the
 // tile does not exist).
+struct Tile {
+    int row0, head, hi, lo;
+};
 struct Pair {
-    int row0[2], head[2], hi[2], lo[2];
+    Tile a, b;
     int top, bottom;  // key tiles of either
 };
 template <bool PAIR_HEADS>
+__device__ __forceinline__ Tile tile_of(const Seq& sq, int unit_head, int window, int s) {
+    Tile t;
+    t.row0 = PAIR_HEADS ? sq.local * kRows : (2 * sq.local + s) * kRows;
+    t.head = PAIR_HEADS ? 2 * unit_head + s : unit_head;
+    t.hi = t.row0 / kRows;
+    t.lo = t.row0 < sq.len ? max(0, t.row0 - window + 1) / kRows : t.hi + 1;
+    return t;
+}
+template <bool PAIR_HEADS>
 __device__ __forceinline__ Pair pair_of(const Seq& sq, int unit_head, int window) {
     Pair pr;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-        pr.row0[s] = PAIR_HEADS ? sq.local * kRows : (2 * sq.local + s) * kRows;
-        pr.head[s] = PAIR_HEADS ? 2 * unit_head + s : unit_head;
-        pr.hi[s] = pr.row0[s] / kRows;
-        pr.lo[s] = pr.row0[s] < sq.len ? max(0, pr.row0[s] - window + 1) / kRows : pr.hi[s] + 1;
-    }
-    const bool two = pr.hi[1] >= pr.lo[1];
-    pr.top = two ? pr.hi[1] : pr.hi[0];
-    pr.bottom = pr.lo[0];  // the first tile exists, and sees at least as far back
+    pr.a = tile_of<PAIR_HEADS>(sq, unit_head, window, 0);
+    pr.b = tile_of<PAIR_HEADS>(sq, unit_head, window, 1);
+    pr.top = pr.b.hi >= pr.b.lo ? pr.b.hi : pr.a.hi;
+    pr.bottom = pr.a.lo;  // the first tile exists, and sees at least as far back
     return pr;
+}
+
+// The issuing thread's place in the stream of ring tiles.
+template <int D>
+struct RingAt {
+    uint32_t slot = 0, phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == (uint32_t)FwdSmem<D>::kStages) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+    __device__ __forceinline__ bool landed(const Ctx& cx) const { return wait_bar(cx, B_R + slot, phase); }
+};
+
+// S of tile S against the K tile in ring slot `slot`.
+template <int D, int S>
+__device__ __forceinline__ void s_product(const Ctx& cx, uint32_t tbase, uint32_t q_desc, uint32_t ring_k, uint32_t slot) {
+    constexpr uint32_t step = FwdSmem<D>::kTile >> 4;
+    mma_ss_rows<D>(tbase + TM_S + 128 * S, q_desc + S * step, ring_k + slot * step);
+    mma_commit(cx.bars + B_S + S);
+}
+// Tile S's part of key tile kt: P V with V in ring slot v, then S of the next key tile with K in slot k.
+template <int D, int S>
+__device__ __forceinline__ bool tile_step(const Ctx& cx, uint32_t tbase, const Tile& t, int kt, uint32_t q_desc,
+                                          uint32_t ring_k, uint32_t ring_mn, uint32_t v, const RingAt<D>& k,
+                                          uint32_t& parity) {
+    constexpr uint32_t step = FwdSmem<D>::kTile >> 4;
+    if (kt <= t.hi && kt >= t.lo) {
+        const uint32_t vd = ring_mn + v * step;
+        if (!wait_bar(cx, B_PA + S, parity)) return false;
+        tc_fence_after();
+        mma_ts_rows<D, 0, 64>(tbase + TM_O + 128 * S, tbase + TM_S + 128 * S, vd, kt < t.hi);
+        if (!wait_bar(cx, B_PB + S, parity)) return false;
+        tc_fence_after();
+        mma_ts_rows<D, 64, 128>(tbase + TM_O + 128 * S, tbase + TM_S + 128 * S, vd, true);
+        if (kt == t.lo) mma_commit(cx.bars + B_O + S);
+        parity ^= 1u;
+    }
+    if (kt - 1 <= t.hi && kt - 1 >= t.lo) {
+        if (!k.landed(cx)) return false;
+        s_product<D, S>(cx, tbase, q_desc, ring_k, k.slot);  // runs after P V, so it may write over P
+    }
+    return true;
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -112,7 +167,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i == B_P || i == B_P + 1 ? 128 : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i >= B_PA && i < B_O ? 4 : 1);
         *cx.abort_flag = 0;
         mbar_fence_init();
     }
@@ -138,10 +193,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 if (f == 2) break;
                 if (f == 1) continue;
                 const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
-                const int hk = pr.head[0] / G;
+                const int hk = pr.a.head / G;
                 if ((tid & 31) == 0) {
                     auto load = [&](const CUtensorMap* map_, int kt) -> bool {
-                        if (ri >= NS && !wait_bar(cx, B_R_FREE + ri % NS, (ri / NS - 1) & 1)) return false;
+                        if (ri >= NS) {  // the slot's last tile, ri - NS, is free with its pair
+                        const int q = ri > NS ? (ri - NS - 1) >> 1 : 0;
+                        if (!wait_bar(cx, B_R_FREE + (q & 3), (q >> 2) & 1)) return false;
+                    }
                         uint64_t* bar = cx.bars + B_R + ri % NS;
                         mbar_arrive_expect_tx(bar, L::kTile);
                         load_tile<D>(sb + L::ring(ri), map_, bar, hk, sq.begin + kt * kRows);
@@ -151,10 +209,10 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     ok = load(&tm_k, pr.top);  // need not wait for the unit before
                     if (ok && units) ok = wait_bar(cx, B_Q_FREE, (units - 1) & 1);
                     if (ok) {
-                        const bool two = pr.hi[1] >= pr.lo[1];
+                        const bool two = pr.b.hi >= pr.b.lo;
                         mbar_arrive_expect_tx(cx.bars + B_Q, two ? 2 * L::kTile : L::kTile);
-                        load_tile<D>(sb + L::kQ, &tm_q, cx.bars + B_Q, pr.head[0], sq.begin + pr.row0[0]);
-                        if (two) load_tile<D>(sb + L::kQ + L::kTile, &tm_q, cx.bars + B_Q, pr.head[1], sq.begin + pr.row0[1]);
+                        load_tile<D>(sb + L::kQ, &tm_q, cx.bars + B_Q, pr.a.head, sq.begin + pr.a.row0);
+                        if (two) load_tile<D>(sb + L::kQ + L::kTile, &tm_q, cx.bars + B_Q, pr.b.head, sq.begin + pr.b.row0);
                         ++units;
                     }
                     ok = ok && load(&tm_v, pr.top);
@@ -169,51 +227,36 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             __syncwarp();
         } else if (warp == kMmaWarp) {
-            int units = 0, ri = 0, done[2] = {0, 0};  // Q tiles and ring tiles so far; items of either tile
+            // The stream of ring tiles: K, V K, V K, .., V and the next unit's K, ..; a V and the K after it are freed
+            // together, after the K's products.
+            uint32_t q_parity = 0, p0 = 0, p1 = 0, pairs = 0;
+            RingAt<D> at;
+            const uint32_t q_desc = desc_k(sb + L::kQ), ring_k = desc_k(sb + L::kRing), ring_mn = desc_mn(sb + L::kRing);
+            bool first = true;
             for (int k = 0; ok; ++k) {
                 const int f = map.unit(k, heads, true, sq, uh);
                 if (f == 2) break;
                 if (f == 1) continue;
                 const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
                 if ((tid & 31) == 0) {
-                    auto landed = [&](int i) { return wait_bar(cx, B_R + i % NS, (i / NS) & 1); };
-                    auto sees = [&](int s, int kt) { return kt <= pr.hi[s] && kt >= pr.lo[s]; };
-                    // S of tile s against the K tile in ring slot i
-                    auto s_product = [&](int s, int i) {
-                        mma_ss_rows<D>(tbase + TM_S + 128 * s, sb + L::kQ + (uint32_t)s * L::kTile, sb + L::ring(i));
-                        mma_commit(cx.bars + B_S + s);
-                    };
-                    ok = wait_bar(cx, B_Q, units & 1) && landed(ri);
-                    ++units;
+                    ok = wait_bar(cx, B_Q, q_parity) && at.landed(cx);
+                    q_parity ^= 1u;
                     if (ok) {
-                        for (int s = 0; s < 2; ++s)
-                            if (sees(s, pr.top)) s_product(s, ri);
-                        mma_commit(cx.bars + B_R_FREE + ri % NS);
+                        if (pr.top <= pr.a.hi) s_product<D, 0>(cx, tbase, q_desc, ring_k, at.slot);
+                        if (pr.b.hi >= pr.b.lo) s_product<D, 1>(cx, tbase, q_desc, ring_k, at.slot);
+                        if (!first) mma_commit(cx.bars + B_R_FREE + (pairs++ & 3));
+                        first = false;
                         if (pr.top == pr.bottom) mma_commit(cx.bars + B_Q_FREE);
                     }
-                    // key tile kt: V in slot ri + 1, the next K in ri + 2
-                    for (int kt = pr.top; ok && kt >= pr.bottom; --kt, ri += 2) {
-                        if (!(ok = landed(ri + 1))) break;
-                        const bool more = kt > pr.bottom;
-                        bool next_k = false;
-                        for (int s = 0; s < 2; ++s) {
-                            if (sees(s, kt)) {
-                                if (!(ok = wait_bar(cx, B_P + s, done[s] & 1))) break;
-                                tc_fence_after();
-                                mma_ts_rows<D>(tbase + TM_O + 128 * s, tbase + TM_S + 128 * s, sb + L::ring(ri + 1), kt < pr.hi[s]);
-                                mma_commit(cx.bars + B_O + s);
-                                ++done[s];
-                            }
-                            if (more && sees(s, kt - 1)) {
-                                if (!next_k && !(ok = landed(ri + 2))) break;
-                                next_k = true;
-                                s_product(s, ri + 2);  // runs after P V, so it may write over P
-                            }
-                        }
-                        if (!ok) break;
-                        mma_commit(cx.bars + B_R_FREE + (ri + 1) % NS);
-                        if (more) {
-                            mma_commit(cx.bars + B_R_FREE + (ri + 2) % NS);
+                    for (int kt = pr.top; ok && kt >= pr.bottom; --kt) {
+                        at.next();
+                        const uint32_t v = at.slot;
+                        if (!(ok = at.landed(cx))) break;
+                        at.next();  // the next K, of this unit or of the one after
+                        ok = tile_step<D, 0>(cx, tbase, pr.a, kt, q_desc, ring_k, ring_mn, v, at, p0) &&
+                             tile_step<D, 1>(cx, tbase, pr.b, kt, q_desc, ring_k, ring_mn, v, at, p1);
+                        if (ok && kt > pr.bottom) {
+                            mma_commit(cx.bars + B_R_FREE + (pairs++ & 3));
                             if (kt - 1 == pr.bottom) mma_commit(cx.bars + B_Q_FREE);
                         }
                     }
@@ -228,22 +271,20 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = tl + TM_S + 128 * s_, t_o = tl + TM_O + 128 * s_;
         const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
-        int gi = 0;   // items of this tile so far
-        int ri = 0;   // ring tiles so far
+        int gi = 0, units = 0;  // items and units of this tile so far
+        int ri = 0;             // ring tiles so far
         for (int k = 0; ok; ++k) {
             const int f = map.unit(k, heads, true, sq, uh);
             if (f == 2) break;
             if (f == 1) continue;
             const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
-            const int row0 = pr.row0[s_], hi = pr.hi[s_], lo = pr.lo[s_];
+            const Tile me = tile_of<PAIR_HEADS>(sq, uh, p.window, s_);
+            const int row0 = me.row0, hi = me.hi, lo = me.lo;
             const int row = row0 + lane;
             float m = -INFINITY, l = 0.f;
             for (int kt = hi; kt >= lo; --kt, ++gi) {
                 if (!(ok = wait_warp(cx, B_S + s_, gi & 1))) break;
-                // P V of the tile before finished earlier (S was issued after it): its phase is seen here, so
-                // that this thread is never two phases behind
-                if (kt < hi && !(ok = wait_warp(cx, B_O + s_, (gi - 1) & 1))) break;
-                tc_fence_after();
+                tc_fence_after();  // P V of the tile before is complete as well: S was issued after it
                 uint32_t s[4][32];
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s[c]);
@@ -291,39 +332,44 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
+                        const f2 y = f2_fma(f2_of(s[c][2 * e], s[c][2 * e + 1]), scale2, nm);
+                        const f2 x = (e & 7) < kPoly ? exp2_pair<true>(y) : exp2_pair<false>(y);
+                        sum[e & 1] = f2_add(sum[e & 1], x);
                         float a, b;
-                        f2_get(f2_fma(f2_of(s[c][2 * e], s[c][2 * e + 1]), scale2, nm), a, b);
-                        a = exp2_approx(a);
-                        b = exp2_approx(b);
-                        sum[e & 1] = f2_add(sum[e & 1], f2_of(a, b));
+                        f2_get(x, a, b);
                         w[e] = pack_bf16x2(a, b);
                     }
                     tmem_st16(t_s + 16 * c, w);
+                    if (c == 1) {
+                        if (kt == hi && sq.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
+                            // V's rows past the sequence: p is 0 there, but 0 * NaN is not.  Two heads share the
+                            // tile, whose product with P1 follows the one with P0.
+                            const int slot = ri + 2 * (pr.top - kt) + 1;
+                            if (!(ok = wait_warp(cx, B_R + slot % NS, (slot / NS) & 1))) break;
+                            if (lane >= sq.len - key0) zero_row<D>(sm + L::ring(slot), lane);
+                            fence_async_shared();
+                        }
+                        tmem_st_wait();
+                        arrive_warp(cx, B_PA + s_);
+                    }
                 }
+                if (!ok) break;
+                tmem_st_wait();
+                arrive_warp(cx, B_PB + s_);
                 float a, b;
                 f2_get(f2_add(sum[0], sum[1]), a, b);
                 l += a + b;
-                if (kt == hi && sq.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
-                    // V's rows past the sequence: p is 0 there, but 0 * NaN is not.  Two heads share the tile,
-                    // whose product with P1 follows the one with P0.
-                    const int slot = ri + 2 * (pr.top - kt) + 1;
-                    if (!(ok = wait_warp(cx, B_R + slot % NS, (slot / NS) & 1))) break;
-                    if (lane >= sq.len - key0) zero_row<D>(sm + L::ring(slot), lane);
-                    fence_async_shared();
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive(cx.bars + B_P + s_);
             }
             ri += 2 * (pr.top - pr.bottom + 1);
             if (!ok) break;
             if (hi < lo) continue;
-            if (!(ok = wait_warp(cx, B_O + s_, (gi - 1) & 1))) break;
+            if (!(ok = wait_warp(cx, B_O + s_, units & 1))) break;
+            ++units;
             tc_fence_after();
             // the next unit's first product into O waits for its P, which follows this
             const bool live = row < sq.len;
             const float inv = 1.f / l;
-            const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + pr.head[s_]) * D;
+            const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + me.head) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -344,7 +390,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // every row of the tile, so that the backward's copies of it read no uninitialised memory
             if (SAVE) {
                 const int tile = sq.tile + (PAIR_HEADS ? 0 : s_);
-                p.io.lse[((int64_t)pr.head[s_] * p.tiles + tile) * kRows + lane] = live ? -(m + log2f(l)) : 0.f;
+                p.io.lse[((int64_t)me.head * p.tiles + tile) * kRows + lane] = live ? -(m + log2f(l)) : 0.f;
             }
         }
     }

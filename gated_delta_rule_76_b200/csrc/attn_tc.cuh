@@ -137,20 +137,24 @@ struct Ctx {
     uint64_t wait_ns;
 };
 
-// Bounded wait of one thread; on expiry the error word and the CTA's abort flag are set.
+// Bounded wait of one thread; on expiry the error word and the CTA's abort flag are set.  A try waits in
+// hardware for a while, and most phases complete within the first few: the clock is read only after those.
 __device__ __forceinline__ bool wait_bar(const Ctx& cx, int bar, uint32_t parity) {
     uint64_t* b = cx.bars + bar;
-    if (mbar_try_wait(b, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_sleep(b, parity, 1000u)) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 0;; ++i) {
+        if (mbar_try_wait(b, parity)) return true;
+        if (i < 16) continue;
         if (*cx.abort_flag) return false;
-        if (globaltimer_ns() - t0 > cx.wait_ns) {
+        const uint64_t now = globaltimer_ns();
+        if (!t0) t0 = now;
+        if (now - t0 > cx.wait_ns) {
             *cx.abort_flag = 1;
             atomicOr(cx.err, 1);
             return false;
         }
     }
-    return true;
 }
 // The same by a whole warp, with one answer: tensor-memory instructions that follow need all lanes.
 __device__ __forceinline__ bool wait_warp(const Ctx& cx, int bar, uint32_t parity) {
@@ -171,21 +175,36 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, 
     for (int c = 0; c < D; c += 64) tma3(dst + (uint32_t)(c >> 6) * (kRows * 128u), map, bar, c, head, row);
 }
 
-// D[tmem] (+)= A[tmem, bf16, 128 columns of K] * B with B a row tile taken MN-major (K = its 128
-// rows, N = its D channels).
-template <int D>
-__device__ __forceinline__ void mma_ts_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_smem, bool accumulate) {
-    constexpr uint32_t idesc = idesc_bf16_f32_mn(128, D, false, true);
-    const uint64_t db = sdesc_mn_sw128(b_smem, kRows * 128u);
-#pragma unroll
-    for (int k = 0; k < kRows; k += 16)
-        mma_ts(d_tmem, a_tmem + (uint32_t)(k >> 1), db + (uint64_t)((k * 128) >> 4), idesc,
-               (accumulate || k > 0) ? 1u : 0u);
+// Shared-memory descriptors of a row tile, as the low word that a tile's address decides and a constant high
+// word (umma.cuh has the fields): K-major, and MN-major with 64-channel groups a box apart.  The issuing thread
+// forms one 32-bit sum a product slice.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k(uint32_t tile) { return (tile >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_mn(uint32_t tile) { return (tile >> 4) | ((kRows * 128u >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kDescHi));
+    return d;
 }
-// D[tmem] = A * B^T for two row tiles (K = channels).
+// D[tmem] (+)= A[tmem, bf16] * B with B a row tile taken MN-major (desc_mn; K = its 128 rows, N = its D
+// channels), for the rows K0 .. K1 - 1; a_tmem is A's column of row 0.
+template <int D, int K0, int K1>
+__device__ __forceinline__ void mma_ts_rows(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_desc, bool accumulate) {
+    constexpr uint32_t idesc = idesc_bf16_f32_mn(128, D, false, true);
+#pragma unroll
+    for (int k = K0; k < K1; k += 16)
+        mma_ts(d_tmem, a_tmem + (uint32_t)(k >> 1), desc_of(b_desc + (uint32_t)((k * 128) >> 4)), idesc,
+               (accumulate || k > K0) ? 1u : 0u);
+}
+// D[tmem] = A * B^T for two row tiles (desc_k; K = channels).
 template <int D>
-__device__ __forceinline__ void mma_ss_rows(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem) {
-    mma_ss_u<D, kRows, kRows>(d_tmem, a_smem, b_smem, idesc_bf16_f32(128, 128), false);
+__device__ __forceinline__ void mma_ss_rows(uint32_t d_tmem, uint32_t a_desc, uint32_t b_desc) {
+    constexpr uint32_t idesc = idesc_bf16_f32(128, 128);
+#pragma unroll
+    for (int k = 0; k < D; k += 16) {
+        const uint32_t o = ((uint32_t)(k >> 6) * kRows * 128u + (uint32_t)(k & 63) * 2u) >> 4;
+        mma_ss(d_tmem, desc_of(a_desc + o), desc_of(b_desc + o), idesc, k > 0 ? 1u : 0u);
+    }
 }
 
 // Zeroes row `row` of a row tile (whole 128-byte lines, so the swizzle does not matter).
@@ -234,6 +253,46 @@ __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// 2^x of a pair on the FMA pipe, for x <= 100 or so: x = n + f with n the nearest integer (found by adding
+// 1.5 * 2^23) and |f| <= 1/2, 2^f by a polynomial, n added to the exponent field.  The polynomial is the
+// minimax one of degree 4 for the relative error with the constant 1 (2^0 = 1 exactly), fitted by reweighted
+// least squares: 2.9e-6 in fp32, far below the 2^-8 of the bf16 weight that the result becomes.  From -127 down the
+// result is 0 (the exponent field of 1, 127, less 127); NaN gives NaN or infinity.
+// The exponential unit computes 16 a cycle and SM, which is as long as the products take: the kernels send a part
+// of the exponentials this way (kPoly).
+__device__ __forceinline__ f2 exp2_poly(f2 x) {
+    float lo, hi;
+    f2_get(x, lo, hi);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-127.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-127.f));
+    x = f2_of(lo, hi);
+    const f2 t = f2_add(x, f2_of(12582912.f, 12582912.f));
+    const f2 f = f2_fma(f2_add(t, f2_of(-12582912.f, -12582912.f)), f2_of(-1.f, -1.f), x);
+    f2 y = f2_fma(f, f2_of(0.009582852945f, 0.009582852945f), f2_of(0.05590642616f, 0.05590642616f));
+    y = f2_fma(f, y, f2_of(0.2402409911f, 0.2402409911f));
+    y = f2_fma(f, y, f2_of(0.6931241751f, 0.6931241751f));
+    y = f2_fma(f, y, f2_of(1.f, 1.f));
+    float n0, n1;
+    f2_get(t, n0, n1);
+    f2_get(y, lo, hi);
+    return f2_of(__float_as_uint(lo) + (__float_as_uint(n0) << 23), __float_as_uint(hi) + (__float_as_uint(n1) << 23));
+}
+// 2^x of a pair, by polynomial or on the exponential unit.
+template <bool POLY>
+__device__ __forceinline__ f2 exp2_pair(f2 x) {
+    if (POLY) return exp2_poly(x);
+    float a, b;
+    f2_get(x, a, b);
+    return f2_of(exp2_approx(a), exp2_approx(b));
+}
+
+// One arrival for a warp, after all its lanes' tensor-memory and shared-memory work.
+__device__ __forceinline__ void arrive_warp(const Ctx& cx, int bar) {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(cx.bars + bar);
 }
 
 // 32 floats of a row into 64 bytes of bf16.
