@@ -155,6 +155,7 @@ AttnIO attn_io(const A* a, void* ws) {
     io.window = a->window;
     io.scale = a->scale;
     io.err = ws_status(ws);
+    io.counters = ws_status(ws) + 2;
     return io;
 }
 void cache_into(AttnIO* io, const void* cache) {
@@ -252,7 +253,7 @@ gdn_status gdn_attn_fwd(const gdn_attn_fwd_args* a, void* workspace, size_t work
     if ((s = check_workspace(workspace, workspace_bytes, gdn_attn_fwd_workspace_size(a)))) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     gdn_attn_fwd_args pa = *a;
-    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, sizeof(int), st);
+    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, 4 * sizeof(int), st);  // the units' counters too
     if (e == cudaSuccess) e = attn_copy(&pa, static_cast<char*>(workspace) + 256, st);
     if (e == cudaSuccess) {
         AttnIO io = attn_io(&pa, workspace);
@@ -289,7 +290,7 @@ gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* a, void* workspace, size_t work
     gdn_attn_bwd_args pa = *a;
     char* ws = static_cast<char*>(workspace);
     const size_t delta = lse_bytes(a->T, a->nseq, a->Hq);
-    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, sizeof(int), st);
+    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, 4 * sizeof(int), st);  // the units' counters too
     if (e == cudaSuccess) e = attn_copy(&pa, ws + 256 + delta, st);
     if (e == cudaSuccess) {
         AttnIO io = attn_io(&pa, workspace);

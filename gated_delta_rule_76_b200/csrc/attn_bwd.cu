@@ -43,13 +43,12 @@ struct BwdSmem {
     static constexpr uint32_t kA = 2 * kTile, kB = 5 * kTile;  // [3] and [2] stages
     static constexpr uint32_t kStats = 7 * kTile;              // dkdv: [2][-lse, -delta][128]
     static constexpr uint32_t kBar = kStats + 2 * 1024;
-    static constexpr uint32_t kBytes = kBar + 176;             // the dynamic array starts on 1024 bytes
+    static constexpr uint32_t kBytes = kBar + 240 + UnitQueue::kBytes;  // the dynamic array starts on 1024 bytes
     static __device__ __forceinline__ uint32_t a(int i) { return kA + (uint32_t)(i % 3) * kTile; }
     static __device__ __forceinline__ uint32_t b(int i) { return kB + (uint32_t)(i & 1) * kTile; }
 };
 static_assert(BwdSmem<128>::kBytes <= 232448, "227 KB");
 constexpr uint32_t TM_S = 0, TM_DP = 128, TM_ACC0 = 256, TM_ACC1 = 384, TM_DS = 384, TM_COLS = 512;
-constexpr int kPoly = 2;  // of 8 exponentials on the FMA pipe
 
 enum BwdBar {
     B_OWN = 0, B_OWN_FREE,      // own tiles landed; read for the last time
@@ -59,9 +58,10 @@ enum BwdBar {
     B_S = B_V_FREE + 2, B_DP,   // products done
     B_X, B_Y, B_DS,             // element-wise steps done (an arrival a warp)
     B_END,                      // the unit's accumulators are complete
-    B_COUNT
+    B_U,                        // UnitQueue
+    B_COUNT = B_U + UnitQueue::kBars
 };
-static_assert(B_COUNT * 8 <= 160, "barriers");
+static_assert(B_COUNT * 8 <= 224, "barriers");
 
 struct BwdParams {
     AttnIO io;
@@ -72,8 +72,8 @@ struct BwdParams {
 // Barriers, tensor memory; false if the shared array does not start where the tiles need it.
 __device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const AttnIO& io, uint32_t*& tmem_slot) {
     cx.bars = reinterpret_cast<uint64_t*>(bars);
-    tmem_slot = reinterpret_cast<uint32_t*>(bars + 160);
-    cx.abort_flag = reinterpret_cast<volatile int*>(bars + 164);
+    tmem_slot = reinterpret_cast<uint32_t*>(bars + 224);
+    cx.abort_flag = reinterpret_cast<volatile int*>(bars + 228);
     cx.err = io.err;
     cx.wait_ns = io.wait_ns ? io.wait_ns : kWaitNs;
     if (smem_u32(sm) & 1023u) {
@@ -81,7 +81,7 @@ __device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const
         return false;
     }
     if (threadIdx.x == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i >= B_X && i <= B_DS ? kElem / 32 : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i >= B_U + 4 ? kElem / 32 + 1 : i >= B_X && i <= B_DS ? kElem / 32 : 1);
         *cx.abort_flag = 0;
         mbar_fence_init();
     }
@@ -173,10 +173,10 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, int h, __nv_bfloat16* 
 }
 
 // Items of a key tile's unit: G heads times the query tiles local .. last that see it.
-__device__ __forceinline__ int query_tiles(const Seq& sq, int window) {
-    const int key0 = sq.local * kRows, reach = sq.len - key0 - kRows;  // rows after the tile
-    const int last = reach < window - 1 ? sq.len - 1 : key0 + kRows - 1 + window - 1;
-    return last / kRows - sq.local + 1;
+__device__ __forceinline__ int query_tiles(const Unit& un, int window) {
+    const int key0 = un.local * kRows, reach = un.len - key0 - kRows;  // rows after the tile
+    const int last = reach < window - 1 ? un.len - 1 : key0 + kRows - 1 + window - 1;
+    return last / kRows - un.local + 1;
 }
 
 template <int D>
@@ -192,22 +192,19 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t* tmem_slot;
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
-    TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
-    Seq sq{};
-    int hk;
+    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, 0};
+    Unit un{};
     bool ok = true;
     int gi = 0;  // items so far, over all units: the stages' and barriers' phases go by it
 
     if (warp == kCopyWarp) {
         int owns = 0, a_items = 0, b_items = 0;  // issued
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, p.io.Hk, false, sq, hk);
-            if (f == 2) break;
-            if (f == 1) continue;
-            const int key0 = sq.begin + sq.local * kRows, nq = query_tiles(sq, p.window), m = G * nq;
+        TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
+        while (units.draw(cx, map, p.io.Hk, false, p.io.counters, un, ok)) {
+            const int key0 = un.begin + un.local * kRows, nq = query_tiles(un, p.window), m = G * nq;
             if ((tid & 31) == 0) {
                 for (int it = 0; ok && it < m; ++it, ++gi) {
-                    const int head = hk * G + it / nq, tile = it % nq;
+                    const int head = un.head * G + it / nq, tile = it % nq;
                     // A's stage was freed with item gi - 3, which the load before this one has waited for
                     uint64_t* bar = cx.bars + B_A + gi % 3;
                     mbar_arrive_expect_tx(bar, L::kTile);
@@ -217,20 +214,20 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     bar = cx.bars + B_B + (gi & 1);
                     mbar_arrive_expect_tx(bar, L::kTile + 2 * kRows * 4);
                     load_tile<D>(sb + L::b(gi), &tm_do, bar, head, key0 + tile * kRows);
-                    const int64_t stat = ((int64_t)head * p.tiles + sq.tile + tile) * kRows;
+                    const int64_t stat = ((int64_t)head * p.tiles + un.tile + tile) * kRows;
                     bulk_g2s(sb + L::kStats + (gi & 1) * 1024u, p.io.lse + stat, kRows * 4, bar);
                     bulk_g2s(sb + L::kStats + (gi & 1) * 1024u + 512u, p.io.delta + stat, kRows * 4, bar);
                     ++b_items;
                     if (it == 0) {  // the first walked tiles need not wait for the unit before
                         if (owns && !(ok = wait_bar(cx, B_OWN_FREE, (owns - 1) & 1))) break;
                         mbar_arrive_expect_tx(cx.bars + B_OWN, 2 * L::kTile);
-                        load_tile<D>(sb + L::kOwn0, &tm_k, cx.bars + B_OWN, hk, key0);
-                        load_tile<D>(sb + L::kOwn1, &tm_v, cx.bars + B_OWN, hk, key0);
+                        load_tile<D>(sb + L::kOwn0, &tm_k, cx.bars + B_OWN, un.head, key0);
+                        load_tile<D>(sb + L::kOwn1, &tm_v, cx.bars + B_OWN, un.head, key0);
                         ++owns;
                     }
                 }
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
         }
         if ((tid & 31) == 0) drain(cx, owns, a_items, b_items);
         __syncwarp();
@@ -241,11 +238,8 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         uint32_t own_phase = 0;
         const uint32_t own0 = desc_k(sb + L::kOwn0), own1 = desc_k(sb + L::kOwn1);
         const uint32_t ak = desc_k(sb + L::kA), bk = desc_k(sb + L::kB), am = desc_mn(sb + L::kA), bm = desc_mn(sb + L::kB);
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, p.io.Hk, false, sq, hk);
-            if (f == 2) break;
-            if (f == 1) continue;
-            const int m = G * query_tiles(sq, p.window);
+        while (units.take(cx, un, ok)) {
+            const int m = G * query_tiles(un, p.window);
             if ((tid & 31) == 0) {
                 auto s_product = [&](const At& i) -> bool {
                     if (!wait_bar(cx, B_A + i.a, i.a_phase)) return false;
@@ -280,19 +274,16 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     nx.next();
                 }
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
         }
         __syncwarp();
     } else {
         const int lane = tid & 127, h = tid >> 7;
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
-        int units = 0;
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, p.io.Hk, false, sq, hk);
-            if (f == 2) break;
-            if (f == 1) continue;
-            const int key0 = sq.local * kRows, nq = query_tiles(sq, p.window), m = G * nq;
+        int done = 0;
+        while (units.take(cx, un, ok)) {
+            const int key0 = un.local * kRows, nq = query_tiles(un, p.window), m = G * nq;
             const int key = key0 + lane;  // within the sequence
             for (int it = 0, tile = 0; it < m; ++it, ++gi, tile = tile + 1 == nq ? 0 : tile + 1) {
                 const int q0 = key0 + tile * kRows;
@@ -306,14 +297,14 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
                 tmem_ld_wait();
                 // rows before the key, past its window or past the sequence
-                const bool tail = q0 + kRows > sq.len;
+                const bool tail = q0 + kRows > un.len;
                 const bool masked = tile == 0 || tail || q0 + kRows - 1 - key0 >= p.window;
                 const int row0 = q0 + 64 * h;
-                const int last = min(p.window - 1 < sq.len ? key + p.window - 1 : sq.len - 1, sq.len - 1) - row0;
+                const int last = min(p.window - 1 < un.len ? key + p.window - 1 : un.len - 1, un.len - 1) - row0;
                 if (tail) {
                     // rows past the sequence have weight 0, but 0 * NaN is not 0; both first products have read them
                     if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
-                    if (lane >= sq.len - q0) zero_row<D>(sm + (h ? L::b(gi) : L::a(gi)), lane);
+                    if (lane >= un.len - q0) zero_row<D>(sm + (h ? L::b(gi) : L::a(gi)), lane);
                     fence_async_shared();
                 }
                 f2 x[32];
@@ -324,8 +315,8 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const float4 l4 = *reinterpret_cast<const float4*>(nlse + 32 * q + 2 * c);
                         const f2 a = f2_fma(f2_of(s[q][2 * c], s[q][2 * c + 1]), scale2, f2_of(l4.x, l4.y));
                         const f2 b = f2_fma(f2_of(s[q][2 * c + 2], s[q][2 * c + 3]), scale2, f2_of(l4.z, l4.w));
-                        x[16 * q + c] = (c & 7) < kPoly ? exp2_pair<true>(a) : exp2_pair<false>(a);
-                        x[16 * q + c + 1] = ((c + 1) & 7) < kPoly ? exp2_pair<true>(b) : exp2_pair<false>(b);
+                        x[16 * q + c] = exp2_pair(a);
+                        x[16 * q + c + 1] = exp2_pair(b);
                     }
                     if (masked) mask_pairs(x + 16 * q, key - row0 - 32 * q, last - 32 * q);
                     st_quarter(tl + TM_S + 64 * h + 16 * q, x + 16 * q);
@@ -358,13 +349,13 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_st_wait();
                 arrive_warp(cx, B_DS);
             }
-            if (!ok || !(ok = wait_warp(cx, B_END, units & 1))) break;
-            ++units;
+            if (!ok || !(ok = wait_warp(cx, B_END, done & 1))) break;
+            ++done;
             tc_fence_after();
             // the next unit's first product into these accumulators waits for its P, which follows this
-            const int64_t at = ((int64_t)(sq.begin + key) * p.io.Hk + hk) * D;
-            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, 1.f, key < sq.len);
-            store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, p.io.scale, key < sq.len);
+            const int64_t at = ((int64_t)(un.begin + key) * p.io.Hk + un.head) * D;
+            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, 1.f, key < un.len);
+            store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, p.io.scale, key < un.len);
         }
     }
     tc_fence_before();
@@ -386,21 +377,18 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     uint32_t* tmem_slot;
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
     const uint32_t tbase = *tmem_slot;
-    TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
-    Seq sq{};
-    int head;
+    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, 0};
+    Unit un{};
     bool ok = true;
     int gi = 0;
     // key tiles of a unit, from the diagonal down to the window's edge
-    auto key_tiles = [&]() { return sq.local - max(0, sq.local * kRows - p.window + 1) / kRows + 1; };
+    auto key_tiles = [&]() { return un.local - max(0, un.local * kRows - p.window + 1) / kRows + 1; };
 
     if (warp == kCopyWarp) {
         int owns = 0, a_items = 0, b_items = 0;  // issued
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, p.io.Hq, true, sq, head);
-            if (f == 2) break;
-            if (f == 1) continue;
-            const int m = key_tiles(), hk = head / G, row0 = sq.begin + sq.local * kRows;
+        TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
+        while (units.draw(cx, map, p.io.Hq, true, p.io.counters + 1, un, ok)) {
+            const int m = key_tiles(), head = un.head, hk = head / G, row0 = un.begin + un.local * kRows;
             if ((tid & 31) == 0) {
                 for (int it = 0; ok && it < m; ++it, ++gi) {
                     const int row = row0 - it * kRows;
@@ -423,7 +411,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
         }
         if ((tid & 31) == 0) drain(cx, owns, a_items, b_items);
         __syncwarp();
@@ -434,10 +422,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         uint32_t own_phase = 0;
         const uint32_t own0 = desc_k(sb + L::kOwn0), own1 = desc_k(sb + L::kOwn1);
         const uint32_t ak = desc_k(sb + L::kA), bk = desc_k(sb + L::kB), am = desc_mn(sb + L::kA);
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, p.io.Hq, true, sq, head);
-            if (f == 2) break;
-            if (f == 1) continue;
+        while (units.take(cx, un, ok)) {
             const int m = key_tiles();
             if ((tid & 31) == 0) {
                 auto s_product = [&](const At& i) -> bool {
@@ -472,20 +457,17 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     nx.next();
                 }
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
         }
         __syncwarp();
     } else {
         const int lane = tid & 127, h = tid >> 7;
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
-        int units = 0;
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, p.io.Hq, true, sq, head);
-            if (f == 2) break;
-            if (f == 1) continue;
-            const int m = key_tiles(), row0 = sq.local * kRows, row = row0 + lane;
-            const int64_t stat = ((int64_t)head * p.tiles + sq.tile) * kRows + lane;
+        int done = 0;
+        while (units.take(cx, un, ok)) {
+            const int m = key_tiles(), row0 = un.local * kRows, row = row0 + lane;
+            const int64_t stat = ((int64_t)un.head * p.tiles + un.tile) * kRows + lane;
             const float nlse = __ldg(p.io.lse + stat), ndelta = __ldg(p.io.delta + stat);
             const f2 nlse2 = f2_of(nlse, nlse), ndelta2 = f2_of(ndelta, ndelta);
             for (int it = 0; it < m; ++it, ++gi) {
@@ -501,7 +483,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int c = 0; c < 32; ++c) {
                     const f2 y = f2_fma(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), scale2, nlse2);
-                    x[c] = (c & 7) < kPoly ? exp2_pair<true>(y) : exp2_pair<false>(y);
+                    x[c] = exp2_pair(y);
                 }
                 // keys after the row or out of its window
                 const bool masked = it == 0 || key0 <= row0 + kRows - 1 - p.window;
@@ -532,19 +514,19 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (gi && !(ok = wait_warp(cx, B_FREE + ((gi - 1) & 3), ((gi - 1) >> 2) & 1))) break;
                 st_quarter(tl + TM_DS + 32 * h, x);
                 st_quarter(tl + TM_DS + 32 * h + 16, x + 16);
-                if (it == 0 && sq.len - key0 < kRows) {
+                if (it == 0 && un.len - key0 < kRows) {
                     // K's rows past the sequence: their ds is 0, but 0 * NaN is not; S is done with them
-                    if (h == 0 && lane >= sq.len - key0) zero_row<D>(sm + L::a(gi), lane);
+                    if (h == 0 && lane >= un.len - key0) zero_row<D>(sm + L::a(gi), lane);
                     fence_async_shared();
                 }
                 tmem_st_wait();
                 arrive_warp(cx, B_DS);
             }
-            if (!ok || !(ok = wait_warp(cx, B_END, units & 1))) break;
-            ++units;
+            if (!ok || !(ok = wait_warp(cx, B_END, done & 1))) break;
+            ++done;
             tc_fence_after();
-            const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + head) * D;
-            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dq) + at, p.io.scale, row < sq.len);
+            const int64_t at = ((int64_t)(un.begin + row) * p.io.Hq + un.head) * D;
+            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dq) + at, p.io.scale, row < un.len);
         }
     }
     tc_fence_before();

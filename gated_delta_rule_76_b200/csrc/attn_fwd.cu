@@ -21,7 +21,9 @@
 // the first half of P V runs under the second half's exponentials.  What bounds: an S product alone reads
 // shared memory at its full 128 bytes a cycle, and the copies write there too; two tiles that share each
 // copy of K and V keep that at 2048 cycles a pair of items, the products' own time.  The exponentials
-// take as long: 16 a cycle and SM.  Every wait is bounded.
+// take as long: 16 a cycle and SM; 3 of 8 of them by a polynomial on the FMA pipe took 514 us instead of 447
+// (a prompt of 16384 tokens), since the softmax's own instructions are what the chain waits for.  Every wait is
+// bounded.
 #include "attn_tc.cuh"
 #include "launch.h"
 #include "tma_host.h"
@@ -41,7 +43,7 @@ struct FwdSmem {
     static constexpr int kStages = D == 128 ? 5 : 10;  // ring of K and V tiles, K(0) V(0) K(1) V(1) ..
     static constexpr uint32_t kTile = kRows * D * 2;
     static constexpr uint32_t kQ = 0, kRing = 2 * kTile, kBar = kRing + kStages * kTile;
-    static constexpr uint32_t kBytes = kBar + 320;  // the dynamic array starts on 1024 bytes
+    static constexpr uint32_t kBytes = kBar + 320 + UnitQueue::kBytes;  // the dynamic array starts on 1024 bytes
     static __device__ __forceinline__ uint32_t ring(int i) { return kRing + (uint32_t)(i % kStages) * kTile; }
 };
 static_assert(FwdSmem<128>::kBytes <= 232448, "227 KB");
@@ -51,12 +53,12 @@ enum FwdBar {
     B_PA = B_S + 2,       // [2] first half of P written (an arrival a warp)
     B_PB = B_PA + 2,      // [2] second half
     B_O = B_PB + 2,       // [2] the unit's last P V done
-    B_R = B_O + 2,        // [stages] landed
+    B_U = B_O + 2,        // UnitQueue
+    B_R = B_U + UnitQueue::kBars,  // [stages] landed
     B_R_FREE = B_R + 10,  // [4] ring tiles 2q + 1 and 2q + 2 read for the last time (q mod 4)
     B_COUNT = B_R_FREE + 4
 };
 static_assert(B_COUNT * 8 <= 304, "barriers");
-constexpr int kPoly = 3;  // of 8 exponentials on the FMA pipe
 // tensor memory: S of either tile, O of either tile
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 
@@ -77,19 +79,19 @@ struct Pair {
     int top, bottom;  // key tiles of either
 };
 template <bool PAIR_HEADS>
-__device__ __forceinline__ Tile tile_of(const Seq& sq, int unit_head, int window, int s) {
+__device__ __forceinline__ Tile tile_of(const Unit& un, int window, int s) {
     Tile t;
-    t.row0 = PAIR_HEADS ? sq.local * kRows : (2 * sq.local + s) * kRows;
-    t.head = PAIR_HEADS ? 2 * unit_head + s : unit_head;
+    t.row0 = PAIR_HEADS ? un.local * kRows : (2 * un.local + s) * kRows;
+    t.head = PAIR_HEADS ? 2 * un.head + s : un.head;
     t.hi = t.row0 / kRows;
-    t.lo = t.row0 < sq.len ? max(0, t.row0 - window + 1) / kRows : t.hi + 1;
+    t.lo = t.row0 < un.len ? max(0, t.row0 - window + 1) / kRows : t.hi + 1;
     return t;
 }
 template <bool PAIR_HEADS>
-__device__ __forceinline__ Pair pair_of(const Seq& sq, int unit_head, int window) {
+__device__ __forceinline__ Pair pair_of(const Unit& un, int window) {
     Pair pr;
-    pr.a = tile_of<PAIR_HEADS>(sq, unit_head, window, 0);
-    pr.b = tile_of<PAIR_HEADS>(sq, unit_head, window, 1);
+    pr.a = tile_of<PAIR_HEADS>(un, window, 0);
+    pr.b = tile_of<PAIR_HEADS>(un, window, 1);
     pr.top = pr.b.hi >= pr.b.lo ? pr.b.hi : pr.a.hi;
     pr.bottom = pr.a.lo;  // the first tile exists, and sees at least as far back
     return pr;
@@ -167,7 +169,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         return;
     }
     if (tid == 0) {
-        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i >= B_PA && i < B_O ? 4 : 1);
+        for (int i = 0; i < B_COUNT; ++i) mbar_init(cx.bars + i, i >= B_U + 4 && i < B_R ? kCopyWarp + 1 : i >= B_PA && i < B_O ? 4 : 1);
         *cx.abort_flag = 0;
         mbar_fence_init();
     }
@@ -179,50 +181,47 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    TileMap<PAIR_HEADS ? kRows : 2 * kRows> map(p.io.cu, p.io.nseq, p.io.T);
-    Seq sq;
-    int uh;
+    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 320), B_U, 0};
+    Unit un{};
     bool ok = true;
 
     if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
         if (warp == kCopyWarp) {
-            int units = 0, ri = 0;  // Q loads and ring loads issued
-            for (int k = 0; ok; ++k) {
-                const int f = map.unit(k, heads, true, sq, uh);
-                if (f == 2) break;
-                if (f == 1) continue;
-                const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
+            int owns = 0, ri = 0;  // Q loads and ring loads issued
+            TileMap<PAIR_HEADS ? kRows : 2 * kRows> map(p.io.cu, p.io.nseq, p.io.T);
+            while (units.draw(cx, map, heads, true, p.io.counters, un, ok)) {
+                const Pair pr = pair_of<PAIR_HEADS>(un, p.window);
                 const int hk = pr.a.head / G;
                 if ((tid & 31) == 0) {
                     auto load = [&](const CUtensorMap* map_, int kt) -> bool {
                         if (ri >= NS) {  // the slot's last tile, ri - NS, is free with its pair
-                        const int q = ri > NS ? (ri - NS - 1) >> 1 : 0;
-                        if (!wait_bar(cx, B_R_FREE + (q & 3), (q >> 2) & 1)) return false;
-                    }
+                            const int q = ri > NS ? (ri - NS - 1) >> 1 : 0;
+                            if (!wait_bar(cx, B_R_FREE + (q & 3), (q >> 2) & 1)) return false;
+                        }
                         uint64_t* bar = cx.bars + B_R + ri % NS;
                         mbar_arrive_expect_tx(bar, L::kTile);
-                        load_tile<D>(sb + L::ring(ri), map_, bar, hk, sq.begin + kt * kRows);
+                        load_tile<D>(sb + L::ring(ri), map_, bar, hk, un.begin + kt * kRows);
                         ++ri;
                         return true;
                     };
                     ok = load(&tm_k, pr.top);  // need not wait for the unit before
-                    if (ok && units) ok = wait_bar(cx, B_Q_FREE, (units - 1) & 1);
+                    if (ok && owns) ok = wait_bar(cx, B_Q_FREE, (owns - 1) & 1);
                     if (ok) {
                         const bool two = pr.b.hi >= pr.b.lo;
                         mbar_arrive_expect_tx(cx.bars + B_Q, two ? 2 * L::kTile : L::kTile);
-                        load_tile<D>(sb + L::kQ, &tm_q, cx.bars + B_Q, pr.a.head, sq.begin + pr.a.row0);
-                        if (two) load_tile<D>(sb + L::kQ + L::kTile, &tm_q, cx.bars + B_Q, pr.b.head, sq.begin + pr.b.row0);
-                        ++units;
+                        load_tile<D>(sb + L::kQ, &tm_q, cx.bars + B_Q, pr.a.head, un.begin + pr.a.row0);
+                        if (two) load_tile<D>(sb + L::kQ + L::kTile, &tm_q, cx.bars + B_Q, pr.b.head, un.begin + pr.b.row0);
+                        ++owns;
                     }
                     ok = ok && load(&tm_v, pr.top);
                     for (int kt = pr.top - 1; ok && kt >= pr.bottom; --kt) ok = load(&tm_k, kt) && load(&tm_v, kt);
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
             }
             if ((tid & 31) == 0 && *cx.abort_flag) {
                 // after an expired wait: the copies still on their way land before the memory is given up
-                if (units) mbar_wait(cx.bars + B_Q, (units - 1) & 1, cx.wait_ns);
+                if (owns) mbar_wait(cx.bars + B_Q, (owns - 1) & 1, cx.wait_ns);
                 for (int i = ri < NS ? 0 : ri - NS; i < ri; ++i) mbar_wait(cx.bars + B_R + i % NS, (i / NS) & 1, cx.wait_ns);
             }
             __syncwarp();
@@ -233,11 +232,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             RingAt<D> at;
             const uint32_t q_desc = desc_k(sb + L::kQ), ring_k = desc_k(sb + L::kRing), ring_mn = desc_mn(sb + L::kRing);
             bool first = true;
-            for (int k = 0; ok; ++k) {
-                const int f = map.unit(k, heads, true, sq, uh);
-                if (f == 2) break;
-                if (f == 1) continue;
-                const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
+            while (units.take(cx, un, ok)) {
+                const Pair pr = pair_of<PAIR_HEADS>(un, p.window);
                 if ((tid & 31) == 0) {
                     ok = wait_bar(cx, B_Q, q_parity) && at.landed(cx);
                     q_parity ^= 1u;
@@ -261,7 +257,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         }
                     }
                 }
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (!(ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0)) break;
             }
             __syncwarp();
         }
@@ -271,14 +267,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         const uint32_t tl = tbase + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t t_s = tl + TM_S + 128 * s_, t_o = tl + TM_O + 128 * s_;
         const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
-        int gi = 0, units = 0;  // items and units of this tile so far
-        int ri = 0;             // ring tiles so far
-        for (int k = 0; ok; ++k) {
-            const int f = map.unit(k, heads, true, sq, uh);
-            if (f == 2) break;
-            if (f == 1) continue;
-            const Pair pr = pair_of<PAIR_HEADS>(sq, uh, p.window);
-            const Tile me = tile_of<PAIR_HEADS>(sq, uh, p.window, s_);
+        int gi = 0, done = 0;  // items and units of this tile so far
+        int ri = 0;            // ring tiles so far
+        while (units.take(cx, un, ok)) {
+            const Pair pr = pair_of<PAIR_HEADS>(un, p.window);
+            const Tile me = s_ ? pr.b : pr.a;
             const int row0 = me.row0, hi = me.hi, lo = me.lo;
             const int row = row0 + lane;
             float m = -INFINITY, l = 0.f;
@@ -333,7 +326,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
                         const f2 y = f2_fma(f2_of(s[c][2 * e], s[c][2 * e + 1]), scale2, nm);
-                        const f2 x = (e & 7) < kPoly ? exp2_pair<true>(y) : exp2_pair<false>(y);
+                        const f2 x = exp2_pair(y);
                         sum[e & 1] = f2_add(sum[e & 1], x);
                         float a, b;
                         f2_get(x, a, b);
@@ -341,12 +334,12 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                     tmem_st16(t_s + 16 * c, w);
                     if (c == 1) {
-                        if (kt == hi && sq.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
+                        if (kt == hi && un.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
                             // V's rows past the sequence: p is 0 there, but 0 * NaN is not.  Two heads share the
                             // tile, whose product with P1 follows the one with P0.
                             const int slot = ri + 2 * (pr.top - kt) + 1;
                             if (!(ok = wait_warp(cx, B_R + slot % NS, (slot / NS) & 1))) break;
-                            if (lane >= sq.len - key0) zero_row<D>(sm + L::ring(slot), lane);
+                            if (lane >= un.len - key0) zero_row<D>(sm + L::ring(slot), lane);
                             fence_async_shared();
                         }
                         tmem_st_wait();
@@ -363,13 +356,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             ri += 2 * (pr.top - pr.bottom + 1);
             if (!ok) break;
             if (hi < lo) continue;
-            if (!(ok = wait_warp(cx, B_O + s_, units & 1))) break;
-            ++units;
+            if (!(ok = wait_warp(cx, B_O + s_, done & 1))) break;
+            ++done;
             tc_fence_after();
             // the next unit's first product into O waits for its P, which follows this
-            const bool live = row < sq.len;
+            const bool live = row < un.len;
             const float inv = 1.f / l;
-            const int64_t at = ((int64_t)(sq.begin + row) * p.io.Hq + me.head) * D;
+            const int64_t at = ((int64_t)(un.begin + row) * p.io.Hq + me.head) * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -389,7 +382,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             // every row of the tile, so that the backward's copies of it read no uninitialised memory
             if (SAVE) {
-                const int tile = sq.tile + (PAIR_HEADS ? 0 : s_);
+                const int tile = un.tile + (PAIR_HEADS ? 0 : s_);
                 p.io.lse[((int64_t)me.head * p.tiles + tile) * kRows + lane] = live ? -(m + log2f(l)) : 0.f;
             }
         }

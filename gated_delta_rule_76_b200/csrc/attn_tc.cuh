@@ -3,8 +3,8 @@
 //
 // Tiles: every sequence is cut into tiles of 128 rows from its own start, and the tiles of all
 // sequences are numbered in order; T / 128 + nseq bounds their number on the host.  CTAs stay for the whole
-// call and find their units of work themselves (TileMap), from cu_seqlens, which the host does not see.  A tile's rows past the end of its
-// sequence belong to others (or to nobody): they are loaded, never stored, and kept out of every
+// call and find their units of work themselves (TileMap, UnitQueue), from cu_seqlens, which the host does not
+// see.  A tile's rows past the end of its sequence belong to others (or to nobody): they are loaded, never stored, and kept out of every
 // sum (masked scores; zeroed rows of operands that a zero weight would multiply, since 0 * NaN is
 // not 0).
 //
@@ -117,17 +117,6 @@ struct TileMap {
             }
         }
     }
-    // Unit k of this CTA's share of `heads` times the tiles: rows of the grid's width in the order above,
-    // every second one backwards, so that the CTAs' sums even out.  0: unit found, 1: none in this row, 2: no more.
-    __device__ __forceinline__ int unit(int k, int heads, bool up, Seq& sq, int& head) {
-        const int64_t at = (int64_t)k * gridDim.x;
-        if (at >= (int64_t)total * heads) return 2;
-        const int64_t u = at + ((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (u >= (int64_t)total * heads) return 1;
-        const uint32_t rank = (uint32_t)u / (uint32_t)heads;  // u < 2^31: the host checks
-        head = (int)((uint32_t)u - rank * (uint32_t)heads);
-        return find((int)rank, up, sq) ? 0 : 2;
-    }
 };
 
 struct Ctx {
@@ -160,6 +149,59 @@ __device__ __forceinline__ bool wait_bar(const Ctx& cx, int bar, uint32_t parity
 __device__ __forceinline__ bool wait_warp(const Ctx& cx, int bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait_bar(cx, bar, parity));
 }
+
+// Units of work (a tile of the order, and a head): the CTA's first is its own number, the others are drawn from a
+// counter in the caller's workspace, which the call has cleared, so that whoever is free takes the heaviest one
+// left.  Results do not depend on who computes them.  The copying warp draws (it runs ahead), finds the tile and
+// passes it on through four slots in shared memory.
+struct Unit {
+    int begin, len;   // the sequence's first token, its tokens
+    int tile, local;  // global number of its (first) 128-row tile, tile within the sequence
+    int head;
+};
+struct UnitQueue {
+    static constexpr uint32_t kBytes = 4 * 32;
+    static constexpr int kBars = 8;  // [4] passed on (an arrival), [4] read (an arrival a reading warp)
+    volatile int* slots;  // [4][8] shared: a Unit, and whether there is one
+    int bar;              // the first of the barriers
+    int n;                // units so far
+    // Drawing side, the whole warp: the next unit; false past the last one, or after an expired wait (then ok is
+    // false too).  The heads of a tile are next to one another; `up` as in TileMap::find.
+    template <int R>
+    __device__ __forceinline__ bool draw(const Ctx& cx, TileMap<R>& map, int heads, bool up, int* counter, Unit& x,
+                                         bool& ok) {
+        if (n >= 4 && !(ok = wait_warp(cx, bar + 4 + (n & 3), ((n >> 2) - 1) & 1))) return false;
+        const bool lead = (threadIdx.x & 31) == 0;
+        int64_t u = blockIdx.x;
+        if (n && lead) u = (int64_t)gridDim.x + atomicAdd(counter, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+        const bool have = u < (int64_t)map.total * heads;  // below 2^31: the host checks
+        if (have) {
+            Seq sq;
+            const uint32_t rank = (uint32_t)u / (uint32_t)heads;
+            map.find((int)rank, up, sq);
+            x = Unit{sq.begin, sq.len, sq.tile, sq.local, (int)((uint32_t)u - rank * (uint32_t)heads)};
+        }
+        if (lead) {
+            volatile int* s = slots + 8 * (n & 3);
+            s[0] = x.begin; s[1] = x.len; s[2] = x.tile; s[3] = x.local; s[4] = x.head; s[5] = have;
+            mbar_arrive(cx.bars + bar + (n & 3));
+        }
+        ++n;
+        return have;
+    }
+    // Reading side, a whole warp: false past the last unit, or after an expired wait (then ok is false too).
+    __device__ __forceinline__ bool take(const Ctx& cx, Unit& x, bool& ok) {
+        if (!(ok = wait_warp(cx, bar + (n & 3), (n >> 2) & 1))) return false;
+        const volatile int* s = slots + 8 * (n & 3);
+        x = Unit{s[0], s[1], s[2], s[3], s[4]};
+        const bool have = s[5] != 0;
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(cx.bars + bar + 4 + (n & 3));
+        ++n;
+        return have;
+    }
+};
 
 __device__ __forceinline__ void tma3(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1, int c2) {
     asm volatile(
@@ -255,34 +297,7 @@ __device__ __forceinline__ float exp2_approx(float x) {
     return y;
 }
 
-// 2^x of a pair on the FMA pipe, for x <= 100 or so: x = n + f with n the nearest integer (found by adding
-// 1.5 * 2^23) and |f| <= 1/2, 2^f by a polynomial, n added to the exponent field.  The polynomial is the
-// minimax one of degree 4 for the relative error with the constant 1 (2^0 = 1 exactly), fitted by reweighted
-// least squares: 2.9e-6 in fp32, far below the 2^-8 of the bf16 weight that the result becomes.  From -127 down the
-// result is 0 (the exponent field of 1, 127, less 127); NaN gives NaN or infinity.
-// The exponential unit computes 16 a cycle and SM, which is as long as the products take: the kernels send a part
-// of the exponentials this way (kPoly).
-__device__ __forceinline__ f2 exp2_poly(f2 x) {
-    float lo, hi;
-    f2_get(x, lo, hi);
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(lo) : "f"(-127.f));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(hi) : "f"(-127.f));
-    x = f2_of(lo, hi);
-    const f2 t = f2_add(x, f2_of(12582912.f, 12582912.f));
-    const f2 f = f2_fma(f2_add(t, f2_of(-12582912.f, -12582912.f)), f2_of(-1.f, -1.f), x);
-    f2 y = f2_fma(f, f2_of(0.009582852945f, 0.009582852945f), f2_of(0.05590642616f, 0.05590642616f));
-    y = f2_fma(f, y, f2_of(0.2402409911f, 0.2402409911f));
-    y = f2_fma(f, y, f2_of(0.6931241751f, 0.6931241751f));
-    y = f2_fma(f, y, f2_of(1.f, 1.f));
-    float n0, n1;
-    f2_get(t, n0, n1);
-    f2_get(y, lo, hi);
-    return f2_of(__float_as_uint(lo) + (__float_as_uint(n0) << 23), __float_as_uint(hi) + (__float_as_uint(n1) << 23));
-}
-// 2^x of a pair, by polynomial or on the exponential unit.
-template <bool POLY>
 __device__ __forceinline__ f2 exp2_pair(f2 x) {
-    if (POLY) return exp2_poly(x);
     float a, b;
     f2_get(x, a, b);
     return f2_of(exp2_approx(a), exp2_approx(b));
