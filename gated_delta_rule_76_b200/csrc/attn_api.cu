@@ -58,6 +58,16 @@ RopeParams rope_of(const gdn_qk_norm& n) {
 }
 Buf freq_buf(const gdn_qk_norm& n) { return {n.inv_freq, (size_t)(n.rot_dim / 2) * 4, "inv_freq"}; }
 
+// Sizes of a paged cache (Hk and d are checked before).
+gdn_status check_cache(int64_t num_pages, int64_t page_size, int64_t max_pages, int64_t Hk, int64_t d) {
+    if (num_pages < 1 || page_size < 1 || max_pages < 1 || num_pages > INT32_MAX || page_size > INT32_MAX ||
+        max_pages > INT32_MAX)
+        return fail(GDN_ERR_INVALID_ARG, "num_pages, page_size and max_pages must be in [1, 2^31)");
+    if (num_pages > (int64_t(1) << 46) / (page_size * Hk * d))  // byte offsets stay within 64 bits
+        return fail(GDN_ERR_UNSUPPORTED, "problem too large: a cache must stay below 2^46 elements");
+    return GDN_OK;
+}
+
 // Shared by the norm-and-rotation calls; k may be absent with Hk = 0.
 template <class A>
 gdn_status check_qk(const A* a) {
@@ -316,9 +326,7 @@ gdn_status gdn_kv_append(const gdn_kv_append_args* a, gdn_stream stream) {
     if (a->Hk < 1) return fail(GDN_ERR_INVALID_ARG, "Hk must be at least 1");
     if (a->nseq < 0 || a->nseq >= kMaxTokens || (!a->cu_seqlens && a->nseq != a->T))
         return fail(GDN_ERR_INVALID_ARG, "nseq=%lld: without cu_seqlens it must be T=%lld", (long long)a->nseq, (long long)a->T);
-    if (a->num_pages < 1 || a->page_size < 1 || a->max_pages < 1 || a->num_pages > INT32_MAX ||
-        a->page_size > INT32_MAX || a->max_pages > INT32_MAX)
-        return fail(GDN_ERR_INVALID_ARG, "num_pages, page_size and max_pages must be in [1, 2^31)");
+    if ((s = check_cache(a->num_pages, a->page_size, a->max_pages, a->Hk, a->d))) return s;
     if (a->T > 0 && (!a->k || !a->v || !a->context_lens || !a->block_table || !a->k_cache || !a->v_cache))
         return fail(GDN_ERR_INVALID_ARG, "k, v, context_lens, block_table, k_cache and v_cache are required");
     if (a->T > 0 && ((a->Hq > 0) != (a->q != nullptr) || (a->Hq > 0) != (a->q_out != nullptr)))
@@ -364,9 +372,8 @@ static gdn_status check_decode_sizes(const gdn_attn_decode_args* a) {
     if (s || (s = check_groups(a->Hq, a->Hk)) || (s = check_scale(a->scale, a->window)) ||
         (s = check_unused(a->strides, false, false)) || (s = check_stride(a->strides.q, a->Hq * a->d, "q")))
         return s;
-    if (a->num_pages < 1 || a->page_size < 1 || a->max_pages < 1 || a->num_pages > INT32_MAX ||
-        a->page_size > INT32_MAX || a->max_pages > INT32_MAX || a->max_context < 0)
-        return fail(GDN_ERR_INVALID_ARG, "num_pages, page_size and max_pages must be in [1, 2^31), max_context >= 0");
+    if ((s = check_cache(a->num_pages, a->page_size, a->max_pages, a->Hk, a->d))) return s;
+    if (a->max_context < 0) return fail(GDN_ERR_INVALID_ARG, "max_context must be >= 0");
     if (a->N * a->Hq >= (int64_t(1) << 22))
         return fail(GDN_ERR_UNSUPPORTED, "problem too large: sequences times heads must stay below 2^22");
     return GDN_OK;

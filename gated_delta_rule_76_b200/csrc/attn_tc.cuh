@@ -51,14 +51,19 @@ struct TileMap {
         }
         return x;
     }
-    // The 32 sequences from s0 on, `before` and `before128` tiles into the batch.
-    __device__ __forceinline__ void load(int s0, int& before, int& before128) {
+    // The 32 sequences from s0 on, `before` and `before128` tiles into the batch, from token `end` on.  Entries
+    // count as the largest so far, within [0, T]: whatever the array holds, the sequences do not overlap, and their
+    // tiles stay within the host's bound.
+    __device__ __forceinline__ void load(int s0, int& before, int& before128, int& end) {
         const int s = s0 + (int)(threadIdx.x & 31);
-        b = e = 0;
-        if (s < nseq) {
-            b = min(max(__ldg(cu + s), 0), T);
-            e = min(max(__ldg(cu + s + 1), b), T);
+        b = max(s < nseq ? min(__ldg(cu + s), T) : 0, end);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, b, o);
+            if ((int)(threadIdx.x & 31) >= o) b = max(b, y);
         }
+        e = max(s < nseq ? min(__ldg(cu + s + 1), T) : 0, b);
+        end = __shfl_sync(0xffffffffu, e, 31);
         t = (e - b + R - 1) / R;
         int incl = scan(t);
         first = before + incl - t;
@@ -74,8 +79,8 @@ struct TileMap {
         }
     }
     __device__ __forceinline__ TileMap(const int32_t* cu_, int nseq_, int T_) : cu(cu_), nseq(nseq_), T(T_) {
-        int before = 0, before128 = 0;
-        for (int s0 = 0; s0 < nseq; s0 += 32) load(s0, before, before128);
+        int before = 0, before128 = 0, end = 0;
+        for (int s0 = 0; s0 < nseq; s0 += 32) load(s0, before, before128, end);
         total = before;
     }
     __device__ __forceinline__ void take(Seq& out, int src, int local) const {
@@ -106,9 +111,9 @@ struct TileMap {
             return true;
         }
         const int g = up ? total - 1 - rank : rank;
-        int before = 0, before128 = 0;
+        int before = 0, before128 = 0, end = 0;
         for (int s0 = 0;; s0 += 32) {
-            load(s0, before, before128);
+            load(s0, before, before128, end);
             const uint32_t hit = __ballot_sync(0xffffffffu, g >= first && g < first + t);
             if (hit) {
                 const int src = __ffs(hit) - 1;

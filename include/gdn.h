@@ -609,7 +609,7 @@ GDN_API gdn_status gdn_attn_decode(const gdn_attn_decode_args* args, void* works
                                    gdn_stream stream);
 
 /* Device-side status of the last call that used `workspace` (a chunk forward, backward or layer
- * core).  The tensor-core kernels bound every internal wait; when one expires the kernel records
+ * core, an attention forward or backward).  The tensor-core kernels bound every internal wait; when one expires the kernel records
  * it in the workspace, stops issuing work, releases its tensor memory and returns.  This call
  * synchronises `stream`, returns GDN_ERR_TIMEOUT if such an expiry was recorded (GDN_OK
  * otherwise) and does not clear the record (the next call on the workspace does). */

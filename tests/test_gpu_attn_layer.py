@@ -1,0 +1,199 @@
+"""The attention layer's calls together, as a training step and a server use them, and what single-operator tests
+do not reach: many units of work per CTA, more sequences than a warp has lanes, calls on two streams at once,
+arrays of sequence starts that no caller should pass."""
+import ctypes
+
+import pytest
+import torch
+
+import attn_ref as ref
+from gated_delta_rule_76_b200 import gdn
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+
+
+def rnd(*s, seed=0, dtype=BF):
+    return torch.randn(*s, generator=torch.Generator().manual_seed(seed)).to(dtype).cuda()
+
+
+def starts(lens):
+    return [sum(lens[:i]) for i in range(len(lens) + 1)]
+
+
+def cache_of(q, k, v, cu):
+    return torch.empty(gdn.gdn_attn_fwd_cache_size(q, k, v, cu), dtype=torch.uint8, device="cuda")
+
+
+def host(t):
+    return ref.f64(t) if t.is_floating_point() else t.cpu()
+
+
+@pytest.mark.parametrize("lens,Hq,Hk,d,window,rot,il", [
+    ([200, 1, 77], 4, 2, 128, 0, 128, False),
+    ([129, 300], 6, 2, 64, 100, 32, True),
+])
+def test_training_step_of_a_layer(lens, Hq, Hk, d, window, rot, il):
+    """One projection buffer's slices through norm and rotation, attention, and both backwards; each stage against
+    the fp64 form over what the stage before it returned, so that only its own roundings count."""
+    T, cu = sum(lens), starts(lens)
+    qkv = rnd(T, (Hq + 2 * Hk) * d, seed=1)
+    q, k, v = (t.unflatten(1, (-1, d)) for t in qkv.split([Hq * d, Hk * d, Hk * d], 1))
+    assert not q.is_contiguous()
+    pos = torch.cat([torch.arange(n) for n in lens]).to(torch.int32).cuda()
+    freq = (10000.0 ** (-torch.arange(0, rot, 2).double() / rot)).float().cuda()
+    qw, kw = ((1 + 0.2 * torch.randn(d, generator=torch.Generator().manual_seed(s))).to(BF).cuda() for s in (2, 3))
+    do = rnd(T, Hq, d, seed=4)
+    norm = dict(q_norm_w=qw, k_norm_w=kw, interleaved=il)
+
+    qr, kr = gdn.gdn_qk_norm_rope_fwd(q, k, pos, freq, **norm)
+    cache = cache_of(qr, kr, v, cu)
+    o = gdn.gdn_attn_fwd(qr, kr, v, cu, window=window, bwd_cache=cache)
+    g = gdn.gdn_attn_bwd(qr, kr, v, cu, o, grad_o=do, fwd_cache=cache, window=window)
+    gx = gdn.gdn_qk_norm_rope_bwd(q, k, pos, freq, grad_q=g["dq"], grad_k=g["dk"], **norm)
+
+    for got, x, w, grad, name in ((qr, q, qw, "dq", "q"), (kr, k, kw, "dk", "k")):
+        a = [host(t) for t in (x, w, pos, freq)]
+        y = ref.norm_rope(*a, interleaved=il)
+        # fp32 arithmetic of a pair (3e-6 of the row's largest, rotated), then one rounding
+        ref.within(got, y, 3e-6 * 2 ** 0.5 * y.abs().amax(-1, keepdim=True) + ref.U * y.abs(), name)
+        dx, dw = ref.norm_rope_grad(*a, host(g[grad]), interleaved=il)
+        r = 1 / torch.sqrt((a[0] ** 2).mean(-1, keepdim=True) + 1e-6)
+        top = host(g[grad]).abs().amax(-1, keepdim=True) * 2 ** 0.5
+        mag = r * a[1].abs().max() * top * (1 + r * r * a[0].abs() * a[0].abs().mean(-1, keepdim=True))
+        ref.within(gx["d" + name], dx, 6e-6 * mag + ref.U * dx.abs(), "d" + name)
+        ref.within(gx[f"d{name}_norm_w"], dw, ref.F * (top * a[0].abs() * r).sum((0, 1)), f"d{name}_norm_w")
+    want, bound, grads, bounds = ref.packed(qr, kr, v, cu, d ** -0.5, window, do)
+    ref.within(o, want, bound, "o")
+    for name, x, b in zip(("dq", "dk", "dv"), grads, bounds):
+        ref.within(g[name], x, b, name)
+
+
+@pytest.mark.parametrize("lens,Hq,Hk,d,window", [
+    ([260] * 20, 8, 2, 64, 0),                                   # about five units a CTA
+    ([131, 1, 0, 7] * 10 + [400], 12, 4, 64, 0),                 # more than 32 sequences; one tile and two
+    ([131, 1, 0, 7] * 10 + [400], 9, 3, 64, 50),                 # an odd group: pairs of tiles, the second often missing
+    ([20] * 300, 3, 1, 64, 0),
+    ([1100], 10, 2, 128, 0),
+    ([1100, 900], 7, 7, 128, 300),
+])
+def test_many_units_a_cta(lens, Hq, Hk, d, window):
+    T, cu = sum(lens), starts(lens)
+    q, k, v, do = (rnd(T, h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk, Hq)))
+    cache = cache_of(q, k, v, cu)
+    o = gdn.gdn_attn_fwd(q, k, v, cu, window=window, bwd_cache=cache)
+    g = gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache, window=window)
+    want, bound, grads, bounds = ref.packed(q, k, v, cu, d ** -0.5, window, do)
+    ref.within(o, want, bound, "o")
+    for name, x, b in zip(("dq", "dk", "dv"), grads, bounds):
+        ref.within(g[name], x, b, name)
+
+
+def test_calls_on_two_streams_at_once():
+    """Two runs of the layer in flight together, each with its own workspace: the same bits as one after the other."""
+    lens, Hq, Hk, d = [500, 300, 41], 8, 2, 128
+    T, cu = sum(lens), torch.tensor(starts(lens), dtype=torch.int32, device="cuda")
+    q, k, v, do = (rnd(T, h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk, Hq)))
+
+    def step(q, stream=None):
+        cache = cache_of(q, k, v, cu)
+        o = gdn.gdn_attn_fwd(q, k, v, cu, bwd_cache=cache, stream=stream)
+        return [o, *gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache, stream=stream).values()]
+
+    inputs = [q, -q]
+    want = [step(x) for x in inputs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in inputs]
+    for _ in range(5):
+        got = []
+        for x, s in zip(inputs, streams):
+            with torch.cuda.stream(s):
+                got.append(step(x))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("cu", [
+    [0, 1280] * 6,                   # overlapping sequences: more tiles than the tokens have
+    [0, 1280] * 40,
+    [0, -7, 900, 300, 1280, 5],
+    [2 ** 31 - 1] * 3, [-2 ** 31, 2 ** 31 - 1],
+])
+def test_malformed_cu_seqlens_write_nothing_but_the_results(cu):
+    """Whatever the device array holds: the buffers' neighbours stay as they were, and the calls end."""
+    T, Hq, Hk, d, pad = 1280, 2, 1, 64, 4096
+    cu = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    q, k, v, do = (rnd(T, h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk, Hq)))
+
+    def guarded(nbytes):
+        whole = torch.full((nbytes + 2 * pad,), 0x5A, dtype=torch.uint8, device="cuda")
+        return whole, whole[pad:pad + nbytes]
+
+    guards = []
+
+    def out(like):
+        whole, mid = guarded(like.numel() * 2)
+        guards.append(whole)
+        return mid.view(BF).view(like.shape)
+
+    whole, cache = guarded(gdn.gdn_attn_fwd_cache_size(q, k, v, cu))
+    guards.append(whole)
+    cache.zero_()
+    o = out(q)
+    gdn.gdn_attn_fwd(q, k, v, cu, o=o, bwd_cache=cache)
+    o.nan_to_num_()
+    ws, room = guarded(1 << 20)
+    guards.append(ws)
+    gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache, dq=out(q), dk=out(k), dv=out(v), workspace=room)
+    torch.cuda.synchronize()
+    for t in guards:
+        assert (t[:pad] == 0x5A).all() and (t[-pad:] == 0x5A).all()
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert gdn.load().gdn_workspace_status(ctypes.c_void_p(room.data_ptr()), st) == 0
+
+
+def test_one_workspace_serves_call_after_call():
+    """The counters of the call before are cleared: a workspace of any contents, used again and again."""
+    lens, Hq, Hk, d = [700, 650], 16, 4, 64
+    q, k, v, do = (rnd(sum(lens), h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk, Hq)))
+    cu = starts(lens)
+    ws = torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    cache = cache_of(q, k, v, cu)
+    o = gdn.gdn_attn_fwd(q, k, v, cu, bwd_cache=cache)
+    g = gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache)
+    for _ in range(3):
+        c2 = cache_of(q, k, v, cu)
+        o2 = gdn.gdn_attn_fwd(q, k, v, cu, bwd_cache=c2, workspace=ws)
+        g2 = gdn.gdn_attn_bwd(q, k, v, cu, o2, grad_o=do, fwd_cache=c2, workspace=ws)
+        assert torch.equal(o, o2) and all(torch.equal(g[n], g2[n]) for n in g)
+
+
+def test_decode_and_append_in_one_graph_replayed():
+    """The captured step of a server: append, attend, advance; replays walk the cache on."""
+    N, Hq, Hk, d, page, steps, rot = 3, 4, 2, 64, 16, 20, 64
+    kc, vc = rnd(20, page, Hk, d, seed=1), rnd(20, page, Hk, d, seed=2)
+    table = torch.randperm(20, generator=torch.Generator().manual_seed(0))[:18].view(N, 6).to(torch.int32).cuda()
+    first = torch.tensor([0, 30, 61], dtype=torch.int32, device="cuda")
+    freq = (10000.0 ** (-torch.arange(0, rot, 2).double() / rot)).float().cuda()
+    toks = [rnd(steps, N, h, d, seed=s) for s, h in ((3, Hq), (4, Hk), (5, Hk))]
+
+    def step(q, k, v, kc, vc, ctx):
+        qs, _ = gdn.gdn_kv_append(k, v, kc, vc, table, ctx, q=q, inv_freq=freq)
+        ctx += 1
+        return gdn.gdn_attn_decode(qs, kc, vc, table, ctx)
+
+    kc1, vc1, ctx1 = kc.clone(), vc.clone(), first.clone()
+    want = [step(*(t[i] for t in toks), kc1, vc1, ctx1) for i in range(steps)]
+    held, ctx = [t[0].clone() for t in toks], first.clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        o = step(*held, kc, vc, ctx)
+    for i in range(steps):
+        for h, t in zip(held, toks):
+            h.copy_(t[i])
+        graph.replay()
+        assert torch.equal(o, want[i]), i
+    assert torch.equal(ctx, ctx1) and torch.equal(kc, kc1) and torch.equal(vc, vc1)
