@@ -157,9 +157,10 @@ __device__ __forceinline__ void mask_pairs(f2* x, int lo, int hi) {
     }
 }
 
-// This thread's part of an accumulator row (half `h` of D columns), times `f`, to dst.
+// Half `h` of the D columns of an accumulator's rows, times `f`, to dst (the warp's first row; rows `stride` elements
+// apart) for the rows below `rows`.
 template <int D>
-__device__ __forceinline__ void store_acc(uint32_t taddr, int h, __nv_bfloat16* dst, float f, bool live) {
+__device__ __forceinline__ void store_acc(uint32_t taddr, int h, __nv_bfloat16* dst, int64_t stride, float f, int rows) {
 #pragma unroll
     for (int c = 0; c < D / 2; c += 32) {
         uint32_t r[32];
@@ -168,7 +169,7 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, int h, __nv_bfloat16* 
         float v[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(r[e]) * f;
-        if (live) store32_bf16(dst + h * (D / 2) + c, v);
+        store_rows(dst + h * (D / 2) + c, stride, v, rows);
     }
 }
 
@@ -353,9 +354,10 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ++done;
             tc_fence_after();
             // the next unit's first product into these accumulators waits for its P, which follows this
-            const int64_t at = ((int64_t)(un.begin + key) * p.io.Hk + un.head) * D;
-            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, 1.f, key < un.len);
-            store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, p.io.scale, key < un.len);
+            const int first = key - (lane & 31);
+            const int64_t stride = (int64_t)p.io.Hk * D, at = (un.begin + first) * stride + un.head * D;
+            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, stride, 1.f, un.len - first);
+            store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, stride, p.io.scale, un.len - first);
         }
     }
     tc_fence_before();
@@ -525,8 +527,9 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if (!ok || !(ok = wait_warp(cx, B_END, done & 1))) break;
             ++done;
             tc_fence_after();
-            const int64_t at = ((int64_t)(un.begin + row) * p.io.Hq + un.head) * D;
-            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dq) + at, p.io.scale, row < un.len);
+            const int first = row - (lane & 31);
+            const int64_t stride = (int64_t)p.io.Hq * D, at = (un.begin + first) * stride + un.head * D;
+            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dq) + at, stride, p.io.scale, un.len - first);
         }
     }
     tc_fence_before();

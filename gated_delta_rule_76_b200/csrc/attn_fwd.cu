@@ -362,7 +362,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             // the next unit's first product into O waits for its P, which follows this
             const bool live = row < un.len;
             const float inv = 1.f / l;
-            const int64_t at = ((int64_t)(un.begin + row) * p.io.Hq + me.head) * D;
+            const int64_t stride = (int64_t)p.io.Hq * D;
+            const int first = row - (lane & 31), rows = un.len - first;  // of the warp
+            const int64_t at = (int64_t)(un.begin + first) * stride + me.head * D;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
@@ -371,13 +373,11 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 float v[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
-                if (live) {
-                    store32_bf16(static_cast<__nv_bfloat16*>(p.io.o) + at + 32 * c, v);
-                    if (SAVE) {
+                store_rows(static_cast<__nv_bfloat16*>(p.io.o) + at + 32 * c, stride, v, rows);
+                if (SAVE) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
-                        store32_bf16(static_cast<__nv_bfloat16*>(p.io.o_lo) + at + 32 * c, v);
-                    }
+                    for (int e = 0; e < 32; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
+                    store_rows(static_cast<__nv_bfloat16*>(p.io.o_lo) + at + 32 * c, stride, v, rows);
                 }
             }
             // every row of the tile, so that the backward's copies of it read no uninitialised memory

@@ -315,16 +315,35 @@ __device__ __forceinline__ void arrive_warp(const Ctx& cx, int bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(cx.bars + bar);
 }
 
-// 32 floats of a row into 64 bytes of bf16.
-__device__ __forceinline__ void store32_bf16(__nv_bfloat16* dst, const float (&x)[32]) {
+// 32 columns of 32 consecutive rows, a row a lane, as bf16 to dst (the first lane's row; rows `stride` elements apart),
+// for the rows below `rows`.  Four lanes exchange their 16-byte pieces first, so that a store writes 64 bytes each of
+// 8 rows: a store of 16 bytes each of 32 rows takes the load/store unit 32 cycles, which the whole CTA waits for at
+// the end of its unit of work.  All lanes.
+__device__ __forceinline__ void store_rows(__nv_bfloat16* dst, int64_t stride, const float (&x)[32], int rows) {
+    const int lane = threadIdx.x & 31;
+    uint32_t w[4][4];  // piece, word
 #pragma unroll
-    for (int i = 0; i < 32; i += 8) {
-        uint4 u;
-        u.x = pack_bf16x2(x[i], x[i + 1]);
-        u.y = pack_bf16x2(x[i + 2], x[i + 3]);
-        u.z = pack_bf16x2(x[i + 4], x[i + 5]);
-        u.w = pack_bf16x2(x[i + 6], x[i + 7]);
-        *reinterpret_cast<uint4*>(dst + i) = u;
+    for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    // transposes the four lanes' pieces: rows and columns 1 apart, then 2
+#pragma unroll
+    for (int o = 1; o <= 2; ++o) {
+        const bool odd = lane & o;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & o) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[c][j] : w[c + o][j], o);
+                if (odd) w[c][j] = got;
+                else w[c + o][j] = got;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = (lane & ~3) + i;
+        if (row < rows)
+            *reinterpret_cast<uint4*>(dst + row * stride + 8 * (lane & 3)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
     }
 }
 
