@@ -300,8 +300,7 @@ gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* a, void* workspace, size_t work
     gdn_attn_bwd_args pa = *a;
     char* ws = static_cast<char*>(workspace);
     const size_t delta = lse_bytes(a->T, a->nseq, a->Hq);
-    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, 4 * sizeof(int), st);  // the units' counters too
-    if (e == cudaSuccess) e = attn_copy(&pa, ws + 256 + delta, st);
+    cudaError_t e = attn_copy(&pa, ws + 256 + delta, st);
     if (e == cudaSuccess) {
         AttnIO io = attn_io(&pa, workspace);
         cache_into(&io, a->fwd_cache);

@@ -22,6 +22,10 @@
 // Shared memory (226 KB): the unit's own two tiles, three stages of the walked tile that S and the last product
 // read (a copy takes about as long as an item, and a stage is held for one and a half), two of the other.
 //
+// The first kernel forms delta; dkdv is set up while it runs, and waits for it.  dq needs nothing from dkdv: its CTAs
+// start as dkdv's end, and fill the SMs that have run out of key tiles (one key head: the first key tile of a long
+// sequence alone takes all of its queries).
+//
 // delta uses o with what its rounding left out (the cache's o_lo): row 0 of a sequence, where do . v - delta
 // cancels, keeps a gradient of 0.  ds and p are rounded to bf16 for the products, nothing else is.
 #include "attn_tc.cuh"
@@ -200,6 +204,8 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (warp == kCopyWarp) {
         int owns = 0, a_items = 0, b_items = 0;  // issued
+        grid_wait();  // the first kernel's sums, and the counters it clears
+        grid_launch_next();
         TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
         while (units.draw(cx, map, p.io.Hk, false, p.io.counters, un, ok)) {
             const int key0 = un.begin + un.local * kRows, nq = query_tiles(un, p.window), m = G * nq;
@@ -377,7 +383,10 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const int G = p.io.Hq / p.io.Hk;
     Ctx cx;
     uint32_t* tmem_slot;
-    if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
+    if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) {
+        grid_wait();
+        return;
+    }
     const uint32_t tbase = *tmem_slot;
     UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, 0};
     Unit un{};
@@ -470,7 +479,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         while (units.take(cx, un, ok)) {
             const int m = key_tiles(), row0 = un.local * kRows, row = row0 + lane;
             const int64_t stat = ((int64_t)un.head * p.tiles + un.tile) * kRows + lane;
-            const float nlse = __ldg(p.io.lse + stat), ndelta = __ldg(p.io.delta + stat);
+            const float nlse = __ldcg(p.io.lse + stat), ndelta = __ldcg(p.io.delta + stat);
             const f2 nlse2 = f2_of(nlse, nlse), ndelta2 = f2_of(ndelta, ndelta);
             for (int it = 0; it < m; ++it, ++gi) {
                 const int key0 = row0 - it * kRows;
@@ -536,6 +545,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tbase, TM_COLS);
+    if (tid == 0) grid_wait();  // what follows this kernel follows dkdv as well
 }
 
 // -delta = -do . (o + o_lo) of every row, tile-aligned like lse (0 for a tile's rows past its sequence).
@@ -543,6 +553,11 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int tiles) {
     constexpr int LANES = D / 8, RPP = 256 / LANES;
+    grid_launch_next();
+    if (blockIdx.x == 0 && threadIdx.x < 2) {
+        if (threadIdx.x == 0) *io.err = 0;
+        io.counters[threadIdx.x] = 0;
+    }
     Seq sq{};
     const int head = blockIdx.x % io.Hq;
     TileMap<kRows> map(io.cu, io.nseq, io.T);
@@ -583,12 +598,23 @@ cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st)
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(attn_dq_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BwdSmem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    attn_dkdv_kernel<D><<<k_tiles < 148 ? k_tiles : 148, kThreads, BwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], maps[3], p);
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(k_tiles < 148 ? k_tiles : 148);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = BwdSmem<D>::kBytes;
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attn_dkdv_kernel<D>, maps[0], maps[1], maps[2], maps[3], p);
     count_launch();
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    attn_dq_kernel<D><<<q_tiles < 148 ? q_tiles : 148, kThreads, BwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], maps[3], p);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(q_tiles < 148 ? q_tiles : 148);
+    e = cudaLaunchKernelEx(&cfg, attn_dq_kernel<D>, maps[0], maps[1], maps[2], maps[3], p);
     count_launch();
-    return cudaGetLastError();
+    return e;
 }
 
 }  // namespace

@@ -155,6 +155,11 @@ __device__ __forceinline__ bool wait_warp(const Ctx& cx, int bar, uint32_t parit
     return __all_sync(0xffffffffu, wait_bar(cx, bar, parity));
 }
 
+// Kernels launched ahead of the end of the one before them in the stream: that one lets it happen, once its CTAs
+// are all running; this one waits until it is complete and its writes are visible.
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Units of work (a tile of the order, and a head): the CTA's first is its own number, the others are drawn from a
 // counter in the caller's workspace, which the call has cleared, so that whoever is free takes the heaviest one
 // left.  Results do not depend on who computes them.  The copying warp draws (it runs ahead), finds the tile and
