@@ -196,16 +196,16 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     Ctx cx;
     uint32_t* tmem_slot;
     if (!setup(cx, sm, sm + L::kBar, p.io, tmem_slot)) return;
+    grid_wait();  // for delta, and the counters
+    grid_launch_next();
     const uint32_t tbase = *tmem_slot;
-    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, 0};
+    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, true, 0};
     Unit un{};
     bool ok = true;
     int gi = 0;  // items so far, over all units: the stages' and barriers' phases go by it
 
     if (warp == kCopyWarp) {
         int owns = 0, a_items = 0, b_items = 0;  // issued
-        grid_wait();  // the first kernel's sums, and the counters it clears
-        grid_launch_next();
         TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
         while (units.draw(cx, map, p.io.Hk, false, p.io.counters, un, ok)) {
             const int key0 = un.begin + un.local * kRows, nq = query_tiles(un, p.window), m = G * nq;
@@ -388,7 +388,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         return;
     }
     const uint32_t tbase = *tmem_slot;
-    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, 0};
+    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 240), B_U, false, 0};
     Unit un{};
     bool ok = true;
     int gi = 0;

@@ -181,7 +181,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_slot;
-    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 320), B_U, 0};
+    UnitQueue units{reinterpret_cast<volatile int*>(sm + L::kBar + 320), B_U, true, 0};
     Unit un{};
     bool ok = true;
 

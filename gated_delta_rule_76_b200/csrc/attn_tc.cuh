@@ -160,9 +160,8 @@ __device__ __forceinline__ bool wait_warp(const Ctx& cx, int bar, uint32_t parit
 __device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Units of work (a tile of the order, and a head): the CTA's first is its own number, the others are drawn from a
-// counter in the caller's workspace, which the call has cleared, so that whoever is free takes the heaviest one
-// left.  Results do not depend on who computes them.  The copying warp draws (it runs ahead), finds the tile and
+// Units of work (a tile of the order, and a head), drawn from a counter in the caller's workspace, which the call
+// has cleared, so that whoever is free takes the heaviest one left.  Results do not depend on who computes them.  The copying warp draws (it runs ahead), finds the tile and
 // passes it on through four slots in shared memory.
 struct Unit {
     int begin, len;   // the sequence's first token, its tokens
@@ -174,6 +173,8 @@ struct UnitQueue {
     static constexpr int kBars = 8;  // [4] passed on (an arrival), [4] read (an arrival a reading warp)
     volatile int* slots;  // [4][8] shared: a Unit, and whether there is one
     int bar;              // the first of the barriers
+    bool own;             // whether the CTA's first unit is its own number: not where a grid's CTAs start late, one by
+                          // one, and would find the heaviest units still waiting for them
     int n;                // units so far
     // Drawing side, the whole warp: the next unit; false past the last one, or after an expired wait (then ok is
     // false too).  The heads of a tile are next to one another; `up` as in TileMap::find.
@@ -183,7 +184,7 @@ struct UnitQueue {
         if (n >= 4 && !(ok = wait_warp(cx, bar + 4 + (n & 3), ((n >> 2) - 1) & 1))) return false;
         const bool lead = (threadIdx.x & 31) == 0;
         int64_t u = blockIdx.x;
-        if (n && lead) u = (int64_t)gridDim.x + atomicAdd(counter, 1);
+        if (lead && (n || !own)) u = (own ? (int64_t)gridDim.x : 0) + atomicAdd(counter, 1);
         u = __shfl_sync(0xffffffffu, u, 0);
         const bool have = u < (int64_t)map.total * heads;  // below 2^31: the host checks
         if (have) {
