@@ -85,7 +85,7 @@ struct AttnIO {
     void *dq, *dk, *dv;
     float* delta;              // [Hq][tiles][128]: rows' -sum of grad_o .* o
     int* err;                  // device error word
-    int* counters;             // [2] zero: the units drawn so far (forward and dkdv; dq)
+    int* counters;             // [2] the units drawn so far (forward and dkdv; dq)
     uint64_t wait_ns;          // limit of one bounded wait, 0: the default
 };
 // Tiles of 128 rows over all sequences, at most.

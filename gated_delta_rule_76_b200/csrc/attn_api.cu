@@ -263,8 +263,7 @@ gdn_status gdn_attn_fwd(const gdn_attn_fwd_args* a, void* workspace, size_t work
     if ((s = check_workspace(workspace, workspace_bytes, gdn_attn_fwd_workspace_size(a)))) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     gdn_attn_fwd_args pa = *a;
-    cudaError_t e = cudaMemsetAsync(ws_status(workspace), 0, 4 * sizeof(int), st);  // the units' counters too
-    if (e == cudaSuccess) e = attn_copy(&pa, static_cast<char*>(workspace) + 256, st);
+    cudaError_t e = attn_copy(&pa, static_cast<char*>(workspace) + 256, st);
     if (e == cudaSuccess) {
         AttnIO io = attn_io(&pa, workspace);
         io.o = a->o;

@@ -164,6 +164,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     cx.abort_flag = reinterpret_cast<volatile int*>(sm + L::kBar + 308);
     cx.err = p.io.err;
     cx.wait_ns = p.io.wait_ns ? p.io.wait_ns : kWaitNs;
+    if (blockIdx.x == 0 && tid == 0) *cx.err = 0;  // every CTA is running, and none gives up a wait within microseconds
     if (sb & 1023u) {
         if (tid == 0) atomicOr(cx.err, 1);
         return;
@@ -394,7 +395,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 }
 
 template <int D, bool SAVE, bool PAIR_HEADS>
-cudaError_t launch(const CUtensorMap* maps, const FwdParams& p, cudaStream_t st) {
+cudaError_t launch(const CUtensorMap* maps, FwdParams p, cudaStream_t st) {
     auto kernel = attn_fwd_kernel<D, SAVE, PAIR_HEADS>;
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdSmem<D>::kBytes);
@@ -403,6 +404,8 @@ cudaError_t launch(const CUtensorMap* maps, const FwdParams& p, cudaStream_t st)
     if (e != cudaSuccess) return e;
     if (attr.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // setmaxnreg counts on them
     const int64_t units = (int64_t)p.tiles * p.io.Hq / (PAIR_HEADS ? 2 : 1);
+    if (units <= 148) p.io.counters = nullptr;  // a unit a CTA
+    else if ((e = cudaMemsetAsync(p.io.counters, 0, sizeof(int), st)) != cudaSuccess) return e;
     kernel<<<(unsigned)(units < 148 ? units : 148), kThreads, FwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], p);
     count_launch();
     return cudaGetLastError();

@@ -176,7 +176,7 @@ struct UnitQueue {
     bool own;             // whether the CTA's first unit is its own number: not where a grid's CTAs start late, one by
                           // one, and would find the heaviest units still waiting for them
     int n;                // units so far
-    // Drawing side, the whole warp: the next unit; false past the last one, or after an expired wait (then ok is
+    // Drawing side, the whole warp (counter: NULL where there is a unit a CTA at most): the next unit; false past the last one, or after an expired wait (then ok is
     // false too).  The heads of a tile are next to one another; `up` as in TileMap::find.
     template <int R>
     __device__ __forceinline__ bool draw(const Ctx& cx, TileMap<R>& map, int heads, bool up, int* counter, Unit& x,
@@ -184,7 +184,10 @@ struct UnitQueue {
         if (n >= 4 && !(ok = wait_warp(cx, bar + 4 + (n & 3), ((n >> 2) - 1) & 1))) return false;
         const bool lead = (threadIdx.x & 31) == 0;
         int64_t u = blockIdx.x;
-        if (lead && (n || !own)) u = (own ? (int64_t)gridDim.x : 0) + atomicAdd(counter, 1);
+        if (n || !own) {
+            u = INT32_MAX;
+            if (lead && counter) u = (own ? (int64_t)gridDim.x : 0) + atomicAdd(counter, 1);
+        }
         u = __shfl_sync(0xffffffffu, u, 0);
         const bool have = u < (int64_t)map.total * heads;  // below 2^31: the host checks
         if (have) {

@@ -627,6 +627,10 @@ def gdn_layer_core_bwd(xq, xk, xv, conv_w, alpha, z, grad_y, b=None, w=None, bet
 # keeps to plain comparisons, and builds its structs from positional values.
 # ---------------------------------------------------------------------------------------------
 _AS_IS = contextlib.nullcontext()
+# what torch.cuda.current_device and current_stream come down to once CUDA is up, as it is where a CUDA tensor exists
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
 def _on(t: torch.Tensor, stream):
@@ -635,14 +639,17 @@ def _on(t: torch.Tensor, stream):
     if not t.is_cuda:
         raise GdnError("libgdn takes CUDA tensors only (there is no CPU path)")
     if stream is None:
-        return _AS_IS if t.get_device() == torch.cuda.current_device() else torch.cuda.device(t.device)
+        return _AS_IS if t.get_device() == _current_device() else torch.cuda.device(t.device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
     return torch.cuda.stream(stream)
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _unexpected(name, t, shape, dtype, device):
+    return GdnError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}: expected "
+                    f"{'' if shape is None else tuple(shape)} {dtype} on cuda:{device}")
 
 
 def _dense(name: str, t: Optional[torch.Tensor], shape, dtype, device: int):
@@ -650,20 +657,34 @@ def _dense(name: str, t: Optional[torch.Tensor], shape, dtype, device: int):
     if t is None:
         return None
     if (shape is not None and t.shape != shape) or t.dtype != dtype or t.get_device() != device:
-        raise GdnError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}: expected "
-                       f"{'' if shape is None else tuple(shape)} {dtype} on cuda:{device}")
+        raise _unexpected(name, t, shape, dtype, device)
     if not t.is_contiguous():
         raise GdnError("libgdn takes contiguous tensors")
     return t.data_ptr()
 
 
-def _packed(name: str, t: torch.Tensor, shape, dtype, device: int):
-    """(address, token stride) of packed tokens [T, heads, d]; shape: what is known of it (-1: any)."""
-    if t.dim() != 3 or any(n not in (-1, m) for n, m in zip(shape, t.shape)) or t.dtype != dtype or t.get_device() != device:
-        raise GdnError(f"{name} is {tuple(t.shape)} {t.dtype} on {t.device}: expected {tuple(shape)} {dtype} on cuda:{device}")
-    if t.is_contiguous():
-        return t.data_ptr(), 0
-    return t.data_ptr(), _token_stride(t.shape, t.stride(), 1)
+def _result(name: str, t: Optional[torch.Tensor], like: torch.Tensor, dtype, device: int):
+    """(the caller's buffer for a result laid out like `like`, or a new one; its address)."""
+    if t is None:
+        t = torch.empty_like(like, memory_format=torch.contiguous_format)
+        return t, t.data_ptr()
+    return t, _dense(name, t, like.shape, dtype, device)
+
+
+def _first(name: str, t: torch.Tensor):
+    """(device, dtype, T, heads, d, token stride) of the packed tokens [T, heads, d] that the others go by."""
+    shape = t.shape
+    if len(shape) != 3:
+        raise GdnError(f"{name} has shape {tuple(shape)}: expected [tokens, heads, channels]")
+    return (t.get_device(), t.dtype, *shape, 0 if t.is_contiguous() else _token_stride(shape, t.stride(), 1))
+
+
+def _packed(name: str, t: torch.Tensor, T: int, d: int, dtype, device: int):
+    """(heads, token stride) of packed tokens [T, heads, d]."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or t.dtype != dtype or t.get_device() != device:
+        raise _unexpected(name, t, (T, "heads", d), dtype, device)
+    return shape[1], 0 if t.is_contiguous() else _token_stride(shape, t.stride(), 1)
 
 
 def _bytes(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor]):
@@ -671,7 +692,7 @@ def _bytes(nbytes: int, like: torch.Tensor, workspace: Optional[torch.Tensor]):
     if nbytes == 0:
         return None, None
     if workspace is None or workspace.numel() * workspace.element_size() < nbytes:
-        workspace = like.new_empty((nbytes,), dtype=torch.uint8)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         raise GdnError(f"the workspace must be contiguous and on {like.device}")
     return workspace.data_ptr(), workspace
@@ -705,13 +726,11 @@ def _qk_norm(d, dtype, device, inv_freq, q_norm_w, k_norm_w, norm_eps, interleav
 
 def _qk_inputs(q, k):
     """(device, dtype, T, Hq, Hk, d, q's address, k's, Strides) of packed q and k (or None)."""
-    dev, dtype = q.get_device(), q.dtype
-    pq, sq = _packed("q", q, (-1, -1, -1), dtype, dev)
-    T, Hq, d = q.shape
+    dev, dtype, T, Hq, d, sq = _first("q", q)
     if k is None:
-        return dev, dtype, T, Hq, 0, d, pq, None, Strides(sq)
-    pk, sk = _packed("k", k, (T, -1, d), dtype, dev)
-    return dev, dtype, T, Hq, k.shape[1], d, pq, pk, Strides(sq, sk)
+        return dev, dtype, T, Hq, 0, d, q.data_ptr(), None, Strides(sq)
+    Hk, sk = _packed("k", k, T, d, dtype, dev)
+    return dev, dtype, T, Hq, Hk, d, q.data_ptr(), k.data_ptr(), Strides(sq, sk)
 
 
 def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, k_norm_w=None,
@@ -721,13 +740,13 @@ def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, 
     ``2 * len(inv_freq)`` channels by ``positions`` [T] int32.  Returns (q_out, k_out)."""
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, strides = _qk_inputs(q, k)
-        if q_out is None:
-            q_out = q.new_empty(q.shape)
-        if k_out is None and k is not None:
-            k_out = k.new_empty(k.shape)
-        a = QkFwdArgs(pq, pk, _dense("positions", positions, (T,), torch.int32, dev),
-                      _dense("q_out", q_out, q.shape, dtype, dev),
-                      _dense("k_out", k_out, None if k is None else k.shape, dtype, dev), T, Hq, Hk, d, _dt(q),
+        q_out, pqo = _result("q_out", q_out, q, dtype, dev)
+        pko = None
+        if k is not None:
+            k_out, pko = _result("k_out", k_out, k, dtype, dev)
+        elif k_out is not None:
+            raise GdnError("k_out needs k")
+        a = QkFwdArgs(pq, pk, _dense("positions", positions, (T,), torch.int32, dev), pqo, pko, T, Hq, Hk, d, _dt(q),
                       _qk_norm(d, dtype, dev, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale), strides)
         check(load().gdn_qk_norm_rope_fwd(ctypes.byref(a), _raw_stream(dev)), "gdn_qk_norm_rope_fwd")
     return q_out, k_out
@@ -740,12 +759,12 @@ def gdn_qk_norm_rope_bwd(q, k, positions=None, inv_freq=None, *, grad_q, grad_k=
     Returns dq, dk in the inputs' dtype and dq_norm_w, dk_norm_w [d] fp32 (those that apply)."""
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, strides = _qk_inputs(q, k)
-        out = {"dq": q.new_empty(q.shape)}
+        out = {"dq": _result("dq", None, q, dtype, dev)[0]}
         if k is not None:
-            out["dk"] = k.new_empty(k.shape)
+            out["dk"] = _result("dk", None, k, dtype, dev)[0]
         for name, w in (("dq_norm_w", q_norm_w), ("dk_norm_w", k_norm_w)):
             if w is not None:
-                out[name] = q.new_empty((d,), dtype=torch.float32)
+                out[name] = torch.empty(d, dtype=torch.float32, device=q.device)
         ptr = {name: t.data_ptr() for name, t in out.items()}
         a = QkBwdArgs(pq, pk, _dense("positions", positions, (T,), torch.int32, dev),
                       _dense("grad_q", grad_q, q.shape, dtype, dev),
@@ -769,12 +788,12 @@ def gdn_attn_fwd_cache_size(q, k, v, cu_seqlens) -> int:
 
 def _qkv(q, k, v):
     """(device, dtype, T, Hq, Hk, d, addresses of q, k, v, Strides) of packed q, k, v."""
-    dev, dtype = q.get_device(), q.dtype
-    pq, sq = _packed("q", q, (-1, -1, -1), dtype, dev)
-    T, Hq, d = q.shape
-    pk, sk = _packed("k", k, (T, -1, d), dtype, dev)
-    pv, sv = _packed("v", v, k.shape, dtype, dev)
-    return dev, dtype, T, Hq, k.shape[1], d, pq, pk, pv, Strides(sq, sk, sv)
+    dev, dtype, T, Hq, d, sq = _first("q", q)
+    Hk, sk = _packed("k", k, T, d, dtype, dev)
+    Hv, sv = _packed("v", v, T, d, dtype, dev)
+    if Hv != Hk:
+        raise _unexpected("v", v, k.shape, dtype, dev)
+    return dev, dtype, T, Hq, Hk, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), Strides(sq, sk, sv)
 
 
 def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: int = 0, o=None,
@@ -786,9 +805,8 @@ def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: 
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, pv, strides = _qkv(q, k, v)
         pcu, nseq, cu = _cu_seqlens(cu_seqlens, dev, T)
-        if o is None:
-            o = q.new_empty(q.shape)
-        a = AttnFwdArgs(pq, pk, pv, pcu, _dense("o", o, q.shape, dtype, dev), T, nseq, Hq, Hk, d, window,
+        o, po = _result("o", o, q, dtype, dev)
+        a = AttnFwdArgs(pq, pk, pv, pcu, po, T, nseq, Hq, Hk, d, window,
                         d ** -0.5 if scale is None else scale, _dt(q),
                         _dense("bwd_cache", bwd_cache, None, torch.uint8, dev),
                         0 if bwd_cache is None else bwd_cache.numel(), strides)
@@ -807,12 +825,11 @@ def gdn_attn_bwd(q, k, v, cu_seqlens, o, *, grad_o, fwd_cache: torch.Tensor, sca
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, pv, strides = _qkv(q, k, v)
         pcu, nseq, cu = _cu_seqlens(cu_seqlens, dev, T)
-        dq = q.new_empty(q.shape) if dq is None else dq
-        dk = k.new_empty(k.shape) if dk is None else dk
-        dv = k.new_empty(k.shape) if dv is None else dv
+        dq, pdq = _result("dq", dq, q, dtype, dev)
+        dk, pdk = _result("dk", dk, k, dtype, dev)
+        dv, pdv = _result("dv", dv, v, dtype, dev)
         a = AttnBwdArgs(pq, pk, pv, pcu, _dense("o", o, q.shape, dtype, dev), _dense("grad_o", grad_o, q.shape, dtype, dev),
-                        _dense("dq", dq, q.shape, dtype, dev), _dense("dk", dk, k.shape, dtype, dev),
-                        _dense("dv", dv, k.shape, dtype, dev), T, nseq, Hq, Hk, d, window,
+                        pdq, pdk, pdv, T, nseq, Hq, Hk, d, window,
                         d ** -0.5 if scale is None else scale, _dt(q),
                         _dense("fwd_cache", fwd_cache, None, torch.uint8, dev), fwd_cache.numel(), strides)
         lib = load()
@@ -844,24 +861,22 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, context_lens, *, cu_seqle
     [T,Hq,d], the same norm and rotation of q.  Returns (q_out or None, k_out or None: the keys as
     cached, with ``want_k``)."""
     with _on(k, stream):
-        dev, dtype = k.get_device(), k.dtype
-        pk, sk = _packed("k", k, (-1, -1, -1), dtype, dev)
-        T, Hk, d = k.shape
-        pv, sv = _packed("v", v, k.shape, dtype, dev)
+        dev, dtype, T, Hk, d, sk = _first("k", k)
+        Hv, sv = _packed("v", v, T, d, dtype, dev)
+        if Hv != Hk:
+            raise _unexpected("v", v, k.shape, dtype, dev)
         pcu, nseq, cu = (None, T, None) if cu_seqlens is None else _cu_seqlens(cu_seqlens, dev, T)
         (pkc, pvc, ptab, pctx), pages = _cache_args(k_cache, v_cache, block_table, context_lens, nseq, Hk, d, dtype, dev)
-        pq, sq, Hq = None, 0, 0
+        pq, pqo, pko, sq, Hq = None, None, None, 0, 0
         if q is not None:
-            pq, sq = _packed("q", q, (T, -1, d), dtype, dev)
-            Hq = q.shape[1]
-            if q_out is None:
-                q_out = q.new_empty(q.shape)
+            Hq, sq = _packed("q", q, T, d, dtype, dev)
+            pq = q.data_ptr()
+            q_out, pqo = _result("q_out", q_out, q, dtype, dev)
         elif q_out is not None:
             raise GdnError("q_out needs q")
-        if want_k and k_out is None:
-            k_out = k.new_empty(k.shape)
-        a = KvAppendArgs(pq, pk, pv, pcu, pctx, ptab, _dense("q_out", q_out, None if q is None else q.shape, dtype, dev),
-                         _dense("k_out", k_out, k.shape, dtype, dev), pkc, pvc, T, nseq, Hq, Hk, d, *pages, _dt(k),
+        if want_k or k_out is not None:
+            k_out, pko = _result("k_out", k_out, k, dtype, dev)
+        a = KvAppendArgs(pq, k.data_ptr(), v.data_ptr(), pcu, pctx, ptab, pqo, pko, pkc, pvc, T, nseq, Hq, Hk, d, *pages, _dt(k),
                          _qk_norm(d, dtype, dev, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale),
                          Strides(sq, sk, sv))
         check(load().gdn_kv_append(ctypes.byref(a), _raw_stream(dev)), "gdn_kv_append")
@@ -874,14 +889,11 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, context_lens, *, scale: Op
     tokens each, this one's included.  ``max_context``: a bound on the lengths that the caller knows
     (0: the block table's reach).  Returns o [N,Hq,d]."""
     with _on(q, stream):
-        dev, dtype = q.get_device(), q.dtype
-        pq, sq = _packed("q", q, (-1, -1, -1), dtype, dev)
-        N, Hq, d = q.shape
+        dev, dtype, N, Hq, d, sq = _first("q", q)
         Hk = k_cache.shape[2] if k_cache.dim() == 4 else 0
         (pkc, pvc, ptab, pctx), pages = _cache_args(k_cache, v_cache, block_table, context_lens, N, Hk, d, dtype, dev)
-        if o is None:
-            o = q.new_empty(q.shape)
-        a = AttnDecodeArgs(pq, pkc, pvc, ptab, pctx, _dense("o", o, q.shape, dtype, dev), N, Hq, Hk, d, *pages,
+        o, po = _result("o", o, q, dtype, dev)
+        a = AttnDecodeArgs(q.data_ptr(), pkc, pvc, ptab, pctx, po, N, Hq, Hk, d, *pages,
                            max_context, window, d ** -0.5 if scale is None else scale, _dt(q), Strides(sq))
         lib = load()
         need = lib.gdn_attn_decode_workspace_size(ctypes.byref(a))
