@@ -131,6 +131,12 @@ size_t cache_bytes(int64_t T, int64_t nseq, int64_t Hq, int64_t d) {
     return T > 0 && nseq > 0 ? lse_bytes(T, nseq, Hq) + (size_t)(T * Hq * d) * 2 : 0;
 }
 
+// One of the backward's two arrays of partial sums (none where a unit is one part).
+size_t part_bytes(const gdn_attn_bwd_args* a) {
+    const int parts = attn_bwd_parts(a->T, a->nseq, a->Hq, a->Hk, a->window);
+    return parts > 1 ? align256((size_t)parts * (size_t)(a->T * a->Hk * a->d) * sizeof(float)) : 0;
+}
+
 template <class A>
 gdn_status check_attn(const A* a, Buf* in) {
     if (!a) return fail(GDN_ERR_INVALID_ARG, "args is NULL");
@@ -275,7 +281,8 @@ gdn_status gdn_attn_fwd(const gdn_attn_fwd_args* a, void* workspace, size_t work
 
 size_t gdn_attn_bwd_workspace_size(const gdn_attn_bwd_args* a) {
     if (!a || a->T < 1 || a->T >= kMaxTokens || a->nseq < 0 || a->Hq < 1 || a->Hk < 1 || a->d < 1) return 0;
-    return with_copies(256 + lse_bytes(a->T, a->nseq, a->Hq), attn_copy_bytes(a));
+    if (a->nseq == 0 || a->Hq < a->Hk) return 0;
+    return with_copies(256 + lse_bytes(a->T, a->nseq, a->Hq) + 2 * part_bytes(a), attn_copy_bytes(a));
 }
 
 gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* a, void* workspace, size_t workspace_bytes, gdn_stream stream) {
@@ -299,7 +306,8 @@ gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* a, void* workspace, size_t work
     gdn_attn_bwd_args pa = *a;
     char* ws = static_cast<char*>(workspace);
     const size_t delta = lse_bytes(a->T, a->nseq, a->Hq);
-    cudaError_t e = attn_copy(&pa, ws + 256 + delta, st);
+    const size_t parts = part_bytes(a);
+    cudaError_t e = attn_copy(&pa, ws + 256 + delta + 2 * parts, st);
     if (e == cudaSuccess) {
         AttnIO io = attn_io(&pa, workspace);
         cache_into(&io, a->fwd_cache);
@@ -309,6 +317,8 @@ gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* a, void* workspace, size_t work
         io.dk = a->grad_k;
         io.dv = a->grad_v;
         io.delta = reinterpret_cast<float*>(ws + 256);
+        io.part_dk = reinterpret_cast<float*>(ws + 256 + delta);
+        io.part_dv = reinterpret_cast<float*>(ws + 256 + delta + parts);
         e = attn_bwd(io, (int)a->d, st);
     }
     return e == cudaSuccess ? GDN_OK : cuda_fail(e, "gdn_attn_bwd");

@@ -22,9 +22,11 @@
 // Shared memory (226 KB): the unit's own two tiles, three stages of the walked tile that S and the last product
 // read (a copy takes about as long as an item, and a stage is held for one and a half), two of the other.
 //
+// Where the key tiles' units are few, each is cut into parts (attn.h), whose fp32 sums go through the workspace and are
+// joined in their order by a last kernel.
+//
 // The first kernel forms delta; dkdv is set up while it runs, and waits for it.  dq needs nothing from dkdv: its CTAs
-// start as dkdv's end, and fill the SMs that have run out of key tiles (one key head: the first key tile of a long
-// sequence alone takes all of its queries).
+// start as dkdv's end, and fill the SMs that have run out of key tiles.
 //
 // delta uses o with what its rounding left out (the cache's o_lo): row 0 of a sequence, where do . v - delta
 // cancels, keeps a gradient of 0.  ds and p are rounded to bf16 for the products, nothing else is.
@@ -70,6 +72,7 @@ static_assert(B_COUNT * 8 <= 224, "barriers");
 struct BwdParams {
     AttnIO io;
     int tiles, window;
+    int parts;  // of a key tile's unit
     float scale_log2;
 };
 
@@ -177,11 +180,37 @@ __device__ __forceinline__ void store_acc(uint32_t taddr, int h, __nv_bfloat16* 
     }
 }
 
+// The same half of this thread's row as fp32, to dst.
+template <int D>
+__device__ __forceinline__ void store_part(uint32_t taddr, int h, float* dst, bool live) {
+#pragma unroll
+    for (int c = 0; c < D / 2; c += 32) {
+        uint32_t r[32];
+        tmem_ld32(taddr + h * (D / 2) + c, r);
+        tmem_ld_wait();
+        if (!live) continue;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<uint4*>(dst + h * (D / 2) + c + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+    }
+}
+
 // Items of a key tile's unit: G heads times the query tiles local .. last that see it.
 __device__ __forceinline__ int query_tiles(const Unit& un, int window) {
     const int key0 = un.local * kRows, reach = un.len - key0 - kRows;  // rows after the tile
     const int last = reach < window - 1 ? un.len - 1 : key0 + kRows - 1 + window - 1;
     return last / kRows - un.local + 1;
+}
+
+// Part `part` of a key tile's unit: its items from `first` on, m of them.
+struct Part {
+    int nq, first, m;
+};
+__device__ __forceinline__ Part part_of(const Unit& un, int part, int parts, int G, int window) {
+    const int nq = query_tiles(un, window);
+    const int64_t all = (int64_t)G * nq;
+    const int first = (int)(all * part / parts);
+    return Part{nq, first, (int)(all * (part + 1) / parts) - first};
 }
 
 template <int D>
@@ -207,11 +236,12 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == kCopyWarp) {
         int owns = 0, a_items = 0, b_items = 0;  // issued
         TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
-        while (units.draw(cx, map, p.io.Hk, false, p.io.counters, un, ok)) {
-            const int key0 = un.begin + un.local * kRows, nq = query_tiles(un, p.window), m = G * nq;
+        while (units.draw(cx, map, p.io.Hk * p.parts, false, p.io.counters, un, ok)) {
+            const int hk = un.head / p.parts, key0 = un.begin + un.local * kRows;
+            const Part pt = part_of(un, un.head - hk * p.parts, p.parts, G, p.window);
             if ((tid & 31) == 0) {
-                for (int it = 0; ok && it < m; ++it, ++gi) {
-                    const int head = un.head * G + it / nq, tile = it % nq;
+                for (int it = 0; ok && it < pt.m; ++it, ++gi) {
+                    const int head = hk * G + (pt.first + it) / pt.nq, tile = (pt.first + it) % pt.nq;
                     // A's stage was freed with item gi - 3, which the load before this one has waited for
                     uint64_t* bar = cx.bars + B_A + gi % 3;
                     mbar_arrive_expect_tx(bar, L::kTile);
@@ -228,8 +258,8 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (it == 0) {  // the first walked tiles need not wait for the unit before
                         if (owns && !(ok = wait_bar(cx, B_OWN_FREE, (owns - 1) & 1))) break;
                         mbar_arrive_expect_tx(cx.bars + B_OWN, 2 * L::kTile);
-                        load_tile<D>(sb + L::kOwn0, &tm_k, cx.bars + B_OWN, un.head, key0);
-                        load_tile<D>(sb + L::kOwn1, &tm_v, cx.bars + B_OWN, un.head, key0);
+                        load_tile<D>(sb + L::kOwn0, &tm_k, cx.bars + B_OWN, hk, key0);
+                        load_tile<D>(sb + L::kOwn1, &tm_v, cx.bars + B_OWN, hk, key0);
                         ++owns;
                     }
                 }
@@ -246,7 +276,8 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t own0 = desc_k(sb + L::kOwn0), own1 = desc_k(sb + L::kOwn1);
         const uint32_t ak = desc_k(sb + L::kA), bk = desc_k(sb + L::kB), am = desc_mn(sb + L::kA), bm = desc_mn(sb + L::kB);
         while (units.take(cx, un, ok)) {
-            const int m = G * query_tiles(un, p.window);
+            const int m = part_of(un, un.head % p.parts, p.parts, G, p.window).m;
+            if (m == 0) continue;
             if ((tid & 31) == 0) {
                 auto s_product = [&](const At& i) -> bool {
                     if (!wait_bar(cx, B_A + i.a, i.a_phase)) return false;
@@ -290,9 +321,11 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const f2 scale2 = f2_of(p.scale_log2, p.scale_log2);
         int done = 0;
         while (units.take(cx, un, ok)) {
-            const int key0 = un.local * kRows, nq = query_tiles(un, p.window), m = G * nq;
-            const int key = key0 + lane;  // within the sequence
-            for (int it = 0, tile = 0; it < m; ++it, ++gi, tile = tile + 1 == nq ? 0 : tile + 1) {
+            const int hk = un.head / p.parts, part = un.head - hk * p.parts;
+            const Part pt = part_of(un, part, p.parts, G, p.window);
+            if (pt.m == 0) continue;
+            const int key0 = un.local * kRows, key = key0 + lane;  // within the sequence
+            for (int it = 0, tile = pt.first % pt.nq; it < pt.m; ++it, ++gi, tile = tile + 1 == pt.nq ? 0 : tile + 1) {
                 const int q0 = key0 + tile * kRows;
                 const float* nlse = reinterpret_cast<const float*>(sm + L::kStats + (gi & 1) * 1024) + 64 * h;
                 const float* ndelta = nlse + kRows;
@@ -361,9 +394,15 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tc_fence_after();
             // the next unit's first product into these accumulators waits for its P, which follows this
             const int first = key - (lane & 31);
-            const int64_t stride = (int64_t)p.io.Hk * D, at = (un.begin + first) * stride + un.head * D;
-            store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, stride, 1.f, un.len - first);
-            store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, stride, p.io.scale, un.len - first);
+            const int64_t stride = (int64_t)p.io.Hk * D, at = (un.begin + first) * stride + hk * D;
+            if (p.parts == 1) {
+                store_acc<D>(tl + TM_ACC0, h, static_cast<__nv_bfloat16*>(p.io.dv) + at, stride, 1.f, un.len - first);
+                store_acc<D>(tl + TM_ACC1, h, static_cast<__nv_bfloat16*>(p.io.dk) + at, stride, p.io.scale, un.len - first);
+            } else {
+                const int64_t all = (int64_t)p.io.T * stride, row = at + (lane & 31) * stride;
+                store_part<D>(tl + TM_ACC0, h, p.io.part_dv + part * all + row, key < un.len);
+                store_part<D>(tl + TM_ACC1, h, p.io.part_dk + part * all + row, key < un.len);
+            }
         }
     }
     tc_fence_before();
@@ -587,9 +626,43 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int ti
     }
 }
 
+// dk and dv of a key tile and head from the parts' sums, in their order.  D / 4 lanes a row, 32 rows a block.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(const BwdParams p) {
+    constexpr int LANES = D / 4, RPP = 256 / LANES;
+    grid_wait();
+    Seq sq{};
+    const int hk = blockIdx.x % p.io.Hk;
+    TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
+    if (!map.find((int)(blockIdx.x / p.io.Hk), false, sq)) return;
+    const Unit un{sq.begin, sq.len, sq.tile, sq.local, hk};
+    const int64_t stride = (int64_t)p.io.Hk * D, all = (int64_t)p.io.T * stride;
+    const int c = (threadIdx.x % LANES) * 4;
+#pragma unroll
+    for (int r = threadIdx.x / LANES; r < 32; r += RPP) {
+        const int row = sq.local * kRows + blockIdx.y * 32 + r;
+        if (row >= sq.len) return;
+        const int64_t at = (sq.begin + row) * stride + hk * D + c;
+        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+        for (int s = 0; s < p.parts; ++s) {
+            if (part_of(un, s, p.parts, p.io.Hq / p.io.Hk, p.window).m == 0) continue;  // nothing was written
+            const float4 a = __ldcg(reinterpret_cast<const float4*>(p.io.part_dk + s * all + at));
+            const float4 b = __ldcg(reinterpret_cast<const float4*>(p.io.part_dv + s * all + at));
+            k.x += a.x; k.y += a.y; k.z += a.z; k.w += a.w;
+            v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
+        }
+        const float f = p.io.scale;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.dk) + at) =
+            make_uint2(pack_bf16x2(k.x * f, k.y * f), pack_bf16x2(k.z * f, k.w * f));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.dv) + at) =
+            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    }
+}
+
 template <int D>
 cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st) {
     const unsigned q_tiles = (unsigned)p.tiles * (unsigned)p.io.Hq, k_tiles = (unsigned)p.tiles * (unsigned)p.io.Hk;
+    const unsigned k_units = k_tiles * (unsigned)p.parts;
     attn_delta_kernel<D><<<q_tiles, 256, 0, st>>>(p.io, p.tiles);
     count_launch();
     cudaError_t e = cudaGetLastError();
@@ -602,7 +675,7 @@ cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st)
     early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     early.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(k_tiles < 148 ? k_tiles : 148);
+    cfg.gridDim = dim3(k_units < 148 ? k_units : 148);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = BwdSmem<D>::kBytes;
     cfg.stream = st;
@@ -613,6 +686,12 @@ cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st)
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3(q_tiles < 148 ? q_tiles : 148);
     e = cudaLaunchKernelEx(&cfg, attn_dq_kernel<D>, maps[0], maps[1], maps[2], maps[3], p);
+    count_launch();
+    if (e != cudaSuccess || p.parts == 1) return e;
+    cfg.gridDim = dim3(k_tiles, 4);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p);
     count_launch();
     return e;
 }
@@ -631,6 +710,7 @@ cudaError_t attn_bwd(const AttnIO& io, int d, cudaStream_t st) {
     p.io = io;
     p.tiles = (int)attn_tiles(io.T, io.nseq);
     p.window = io.window > 0 && io.window < INT32_MAX ? (int)io.window : INT32_MAX;
+    p.parts = attn_bwd_parts(io.T, io.nseq, io.Hq, io.Hk, io.window);
     p.scale_log2 = io.scale * 1.4426950408889634f;
     return d == 128 ? attn::launch<128>(maps, p, st) : attn::launch<64>(maps, p, st);
 }

@@ -144,7 +144,7 @@ def test_malformed_cu_seqlens_write_nothing_but_the_results(cu):
     o = out(q)
     gdn.gdn_attn_fwd(q, k, v, cu, o=o, bwd_cache=cache)
     o.nan_to_num_()
-    ws, room = guarded(1 << 20)
+    ws, room = guarded(1 << 25)
     guards.append(ws)
     gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache, dq=out(q), dk=out(k), dv=out(v), workspace=room)
     torch.cuda.synchronize()
@@ -159,7 +159,7 @@ def test_one_workspace_serves_call_after_call():
     lens, Hq, Hk, d = [700, 650], 16, 4, 64
     q, k, v, do = (rnd(sum(lens), h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk, Hq)))
     cu = starts(lens)
-    ws = torch.full((1 << 20,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((1 << 25,), 0xFF, dtype=torch.uint8, device="cuda")
     cache = cache_of(q, k, v, cu)
     o = gdn.gdn_attn_fwd(q, k, v, cu, bwd_cache=cache)
     g = gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache)
