@@ -154,16 +154,6 @@ __device__ __forceinline__ void st_quarter(uint32_t taddr, const f2* x) {
     }
     tmem_st16(taddr, w);
 }
-// Columns outside [lo, hi] to 0.
-__device__ __forceinline__ void mask_pairs(f2* x, int lo, int hi) {
-#pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        float a, b;
-        f2_get(x[c], a, b);
-        x[c] = f2_of(2 * c < lo || 2 * c > hi ? 0.f : a, 2 * c + 1 < lo || 2 * c + 1 > hi ? 0.f : b);
-    }
-}
-
 // Half `h` of the D columns of an accumulator's rows, times `f`, to dst (the warp's first row; rows `stride` elements
 // apart) for the rows below `rows`.
 template <int D>
@@ -340,7 +330,15 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const bool tail = q0 + kRows > un.len;
                 const bool masked = tile == 0 || tail || q0 + kRows - 1 - key0 >= p.window;
                 const int row0 = q0 + 64 * h;
-                const int last = min(p.window - 1 < un.len ? key + p.window - 1 : un.len - 1, un.len - 1) - row0;
+                uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (masked) {
+                    const int last = min(p.window - 1 < un.len ? key + p.window - 1 : un.len - 1, un.len - 1) - row0;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        see[q] = columns(key - row0 - 32 * q, last - 32 * q);
+                        mask_columns(s[q], see[q], kMinusInf);
+                    }
+                }
                 if (tail) {
                     // rows past the sequence have weight 0, but 0 * NaN is not 0; both first products have read them
                     if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
@@ -358,7 +356,6 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         x[16 * q + c] = exp2_pair(a);
                         x[16 * q + c + 1] = exp2_pair(b);
                     }
-                    if (masked) mask_pairs(x + 16 * q, key - row0 - 32 * q, last - 32 * q);
                     st_quarter(tl + TM_S + 64 * h + 16 * q, x + 16 * q);
                     tmem_st_wait();
                     arrive_warp(cx, q ? B_Y : B_X);
@@ -369,13 +366,8 @@ attn_dkdv_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tmem_ld32(tl + TM_DP + 64 * h + 32, s[1]);
                 tmem_ld_wait();
                 if (masked) {  // where the weight is 0, do . v may be anything
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float a, b;
-                        f2_get(x[c], a, b);
-                        if (a == 0.f) s[c >> 4][(2 * c) & 31] = 0u;
-                        if (b == 0.f) s[c >> 4][(2 * c + 1) & 31] = 0u;
-                    }
+                    mask_columns(s[0], see[0], 0u);
+                    mask_columns(s[1], see[1], 0u);
                 }
 #pragma unroll
                 for (int c = 0; c < 32; c += 2) {
@@ -529,19 +521,21 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tmem_ld32(tl + TM_S + 64 * h + 32, s[1]);
                 tmem_ld_wait();
                 arrive_warp(cx, B_X);
-                f2 x[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const f2 y = f2_fma(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), scale2, nlse2);
-                    x[c] = exp2_pair(y);
-                }
                 // keys after the row or out of its window
                 const bool masked = it == 0 || key0 <= row0 + kRows - 1 - p.window;
+                uint32_t see[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
                 if (masked) {
                     const int last = row - key0 - 64 * h;
-                    mask_pairs(x, last - p.window + 1, last);
-                    mask_pairs(x + 16, last - p.window + 1 - 32, last - 32);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        see[q] = columns(last - p.window + 1 - 32 * q, last - 32 * q);
+                        mask_columns(s[q], see[q], kMinusInf);
+                    }
                 }
+                f2 x[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    x[c] = exp2_pair(f2_fma(f2_of(s[c >> 4][(2 * c) & 31], s[c >> 4][(2 * c + 1) & 31]), scale2, nlse2));
                 if (!(ok = wait_warp(cx, B_DP, gi & 1))) break;
                 tc_fence_after();
                 tmem_ld32(tl + TM_DP + 64 * h, s[0]);
@@ -549,13 +543,8 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tmem_ld_wait();
                 arrive_warp(cx, B_Y);
                 if (masked) {  // where the weight is 0, do . v may be anything
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) {
-                        float a, b;
-                        f2_get(x[c], a, b);
-                        if (a == 0.f) s[c >> 4][(2 * c) & 31] = 0u;
-                        if (b == 0.f) s[c >> 4][(2 * c + 1) & 31] = 0u;
-                    }
+                    mask_columns(s[0], see[0], 0u);
+                    mask_columns(s[1], see[1], 0u);
                 }
 #pragma unroll
                 for (int c = 0; c < 32; ++c)

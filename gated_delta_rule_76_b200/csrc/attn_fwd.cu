@@ -286,14 +286,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 const int key0 = kt * kRows;
                 // keys after the row, or out of its window, leave the softmax
                 if (kt == hi || key0 <= row0 + kRows - 1 - p.window) {
-                    const int last = row - key0, gone = last - p.window;
+                    const int last = row - key0;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int j = 32 * c + e;
-                            if (j > last || j <= gone) s[c][e] = 0xFF800000u;  // -inf
-                        }
+                    for (int c = 0; c < 4; ++c) mask_columns(s[c], columns(last - p.window + 1 - 32 * c, last - 32 * c), kMinusInf);
                 }
                 float x[4];
 #pragma unroll
@@ -367,18 +362,22 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const int first = row - (lane & 31), rows = un.len - first;  // of the warp
             const int64_t at = (int64_t)(un.begin + first) * stride + me.head * D;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(t_o + 32 * c, o);
+            for (int c0 = 0; c0 < D; c0 += 64) {
+                uint32_t o[2][32];
+                tmem_ld32(t_o + c0, o[0]);
+                tmem_ld32(t_o + c0 + 32, o[1]);
                 tmem_ld_wait();
-                float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[e]) * inv;
-                store_rows(static_cast<__nv_bfloat16*>(p.io.o) + at + 32 * c, stride, v, rows);
-                if (SAVE) {
+                for (int c = 0; c < 2; ++c) {
+                    float v[32];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
-                    store_rows(static_cast<__nv_bfloat16*>(p.io.o_lo) + at + 32 * c, stride, v, rows);
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(o[c][e]) * inv;
+                    store_rows(static_cast<__nv_bfloat16*>(p.io.o) + at + c0 + 32 * c, stride, v, rows);
+                    if (SAVE) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
+                        store_rows(static_cast<__nv_bfloat16*>(p.io.o_lo) + at + c0 + 32 * c, stride, v, rows);
+                    }
                 }
             }
             // every row of the tile, so that the backward's copies of it read no uninitialised memory

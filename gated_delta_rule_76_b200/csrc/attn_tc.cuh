@@ -317,6 +317,20 @@ __device__ __forceinline__ f2 exp2_pair(f2 x) {
     return f2_of(exp2_approx(a), exp2_approx(b));
 }
 
+// The columns lo .. hi of 32, as bits.
+__device__ __forceinline__ uint32_t columns(int lo, int hi) {
+    if (hi < 0 || lo > 31 || lo > hi) return 0u;
+    return (0xFFFFFFFFu << max(lo, 0)) & (0xFFFFFFFFu >> (31 - min(hi, 31)));
+}
+// Entries without their bit to `fill`.  A warp that has them all skips it.
+__device__ __forceinline__ void mask_columns(uint32_t (&s)[32], uint32_t bits, uint32_t fill) {
+    if (__all_sync(0xffffffffu, bits == 0xFFFFFFFFu)) return;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+        if (!(bits & (1u << e))) s[e] = fill;
+}
+constexpr uint32_t kMinusInf = 0xFF800000u;
+
 // One arrival for a warp, after all its lanes' tensor-memory and shared-memory work.
 __device__ __forceinline__ void arrive_warp(const Ctx& cx, int bar) {
     tc_fence_before();
@@ -348,12 +362,11 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* dst, int64_t stride, c
             }
         }
     }
+    dst += (lane & ~3) * stride + 8 * (lane & 3);
+    rows -= lane & ~3;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int row = (lane & ~3) + i;
-        if (row < rows)
-            *reinterpret_cast<uint4*>(dst + row * stride + 8 * (lane & 3)) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
-    }
+    for (int i = 0; i < 4; ++i, dst += stride)
+        if (i < rows) *reinterpret_cast<uint4*>(dst) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
 }
 
 }  // namespace attn
