@@ -28,6 +28,12 @@
 // The first kernel forms delta; dkdv is set up while it runs, and waits for it.  dq needs nothing from dkdv: its CTAs
 // start as dkdv's end, and fill the SMs that have run out of key tiles.
 //
+// What bounds: dkdv's chain of P, dV, S (about 2980 cycles an item in a long call, of which the products take 2048) and
+// dq's element-wise work (2660 and 1536).  Forward and backward of 4 sequences of 2048, 16 heads of 128 on 4: 333 us, 723
+// TFLOP/s of the formula's 7 products (the kernels compute 9), the tensor pipe active 51% of dkdv and 48% of dq.
+// Tried and slower: dkdv with S in halves, one of them ahead of dV (8%: the narrow products' time); 16 element-wise warps
+// (no difference).
+//
 // delta uses o with what its rounding left out (the cache's o_lo): row 0 of a sequence, where do . v - delta
 // cancels, keeps a gradient of 0.  ds and p are rounded to bf16 for the products, nothing else is.
 #include "attn_tc.cuh"
@@ -577,7 +583,7 @@ attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 }
 
 // -delta = -do . (o + o_lo) of every row, tile-aligned like lse (0 for a tile's rows past its sequence).
-// D / 8 lanes a row, 8 channels each.  HBM bound: three reads of 2 bytes a channel.
+// D / 8 lanes a row, 8 channels each.  HBM bound: three reads of 2 bytes a channel.  A CTA walks its tiles in order.
 template <int D>
 __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int tiles) {
     constexpr int LANES = D / 8, RPP = 256 / LANES;
@@ -586,32 +592,35 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int ti
         if (threadIdx.x == 0) *io.err = 0;
         io.counters[threadIdx.x] = 0;
     }
-    Seq sq{};
-    const int head = blockIdx.x % io.Hq;
     TileMap<kRows> map(io.cu, io.nseq, io.T);
-    if (!map.find((int)(blockIdx.x / io.Hq), false, sq)) return;
     const int c0 = (threadIdx.x % LANES) * 8;
-    const int row0 = sq.local * kRows;
+    const int64_t units = (int64_t)map.total * io.Hq;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        Seq sq{};
+        const int rank = (int)(u / io.Hq), head = (int)(u - (int64_t)rank * io.Hq);
+        if (!map.find(rank, false, sq)) return;
+        const int row0 = sq.local * kRows;
 #pragma unroll
-    for (int r0 = 0; r0 < kRows; r0 += RPP) {
-        const int r = r0 + threadIdx.x / LANES;
-        float sum = 0.f;
-        if (row0 + r < sq.len) {
-            const int64_t at = ((int64_t)(sq.begin + row0 + r) * io.Hq + head) * D + c0;
-            const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(io.grad_o) + at));
-            const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(io.o) + at));
-            const uint4 c = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(io.o_lo) + at));
-            const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w}, z[4] = {c.x, c.y, c.z, c.w};
+        for (int r0 = 0; r0 < kRows; r0 += RPP) {
+            const int r = r0 + threadIdx.x / LANES;
+            float sum = 0.f;
+            if (row0 + r < sq.len) {
+                const int64_t at = ((int64_t)(sq.begin + row0 + r) * io.Hq + head) * D + c0;
+                const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(io.grad_o) + at));
+                const uint4 b = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(io.o) + at));
+                const uint4 c = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(io.o_lo) + at));
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w}, z[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16) + __uint_as_float(z[i] << 16), sum);
-                sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u),
-                           __uint_as_float(y[i] & 0xFFFF0000u) + __uint_as_float(z[i] & 0xFFFF0000u), sum);
+                for (int i = 0; i < 4; ++i) {
+                    sum = fmaf(__uint_as_float(x[i] << 16), __uint_as_float(y[i] << 16) + __uint_as_float(z[i] << 16), sum);
+                    sum = fmaf(__uint_as_float(x[i] & 0xFFFF0000u),
+                               __uint_as_float(y[i] & 0xFFFF0000u) + __uint_as_float(z[i] & 0xFFFF0000u), sum);
+                }
             }
-        }
 #pragma unroll
-        for (int o = LANES / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (c0 == 0) io.delta[((int64_t)head * tiles + sq.tile) * kRows + r] = -sum;
+            for (int o = LANES / 2; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (c0 == 0) io.delta[((int64_t)head * tiles + sq.tile) * kRows + r] = -sum;
+        }
     }
 }
 
@@ -652,7 +661,9 @@ template <int D>
 cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st) {
     const unsigned q_tiles = (unsigned)p.tiles * (unsigned)p.io.Hq, k_tiles = (unsigned)p.tiles * (unsigned)p.io.Hk;
     const unsigned k_units = k_tiles * (unsigned)p.parts;
-    attn_delta_kernel<D><<<q_tiles, 256, 0, st>>>(p.io, p.tiles);
+    // more sequences than a warp holds: few CTAs, which read the array on
+    const unsigned walkers = p.io.nseq > 32 && q_tiles > 148 * 6 ? 148 * 6 : q_tiles;
+    attn_delta_kernel<D><<<walkers, 256, 0, st>>>(p.io, p.tiles);
     count_launch();
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess)

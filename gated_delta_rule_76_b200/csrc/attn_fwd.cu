@@ -16,14 +16,19 @@
 // softmax of either tile, warp 8 copies, warp 9 issues the products, in the order
 //     P0(j) ready: P0 V (j), S0(j+1) | P1(j) ready: P1 V (j), S1(j+1) | ...
 // so the tensor pipe works on one tile while the other's softmax runs.  (One issuer: two let the tiles' products
-// interleave, which lengthens both chains: 381 us against 300 for 8192 tokens, 16 heads.)  A tile's own chain is
-// its softmax, P V, S, and about 460 cycles until a product's end is seen; P goes over in two halves, so that
-// the first half of P V runs under the second half's exponentials.  What bounds: an S product alone reads
-// shared memory at its full 128 bytes a cycle, and the copies write there too; two tiles that share each
-// copy of K and V keep that at 2048 cycles a pair of items, the products' own time.  The exponentials
-// take as long: 16 a cycle and SM; 3 of 8 of them by a polynomial on the FMA pipe took 514 us instead of 447
-// (a prompt of 16384 tokens), since the softmax's own instructions are what the chain waits for.  Every wait is
-// bounded.
+// interleave, which lengthens both chains: 381 us against 300 for 8192 tokens, 16 heads.)  P goes over in two halves, so
+// that the first half of P V runs under the second half's exponentials.  Every wait is bounded.
+//
+// What bounds: a tile's own chain, about 3400 cycles an item on the timestamps: softmax 1750, then until the next S is
+// seen 1650 (the second half of P V 256, S 512, about 490 from a product's last instruction to its barrier, and the
+// waits).  Products alone take 2048 a pair of items (an S product reads shared memory at its full 128 bytes a cycle;
+// the two tiles share each copy of K and V), the exponentials as long (16 a cycle and SM).  A prompt of 16384
+// tokens, 8 heads of 128 on one: 440 us, 1250 TFLOP/s, the tensor pipe active 57% of the time.  At a unit's end the CTA
+// waits about 3500 cycles more for the last P V, the rows on their way out and the first masked tile.
+// Tried and slower: 3 of 8 exponentials by a polynomial on the FMA pipe (514 us instead of 447: the softmax's
+// instructions are in the chain, the exponential unit is not what it waits for); S in steps of 64 keys with two
+// buffers each (636 us: the narrow product takes 386 cycles instead of 256, and every step its own waits); units of one
+// tile where there are few (2600 tokens, 8 heads: 57 us instead of 55).
 #include "attn_tc.cuh"
 #include "launch.h"
 #include "tma_host.h"

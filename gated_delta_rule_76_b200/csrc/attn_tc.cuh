@@ -34,14 +34,17 @@ struct Seq {
 // warp-collective).  With up to 32 sequences the tiles come in descending order of their work: a tile of a
 // causal sequence of t tiles has 1, 2, .. or t tiles to look at, one tile of each (a window caps the larger
 // ones, which keeps the order), so the r-th heaviest is found by counting.  With more sequences they come in the
-// sequences' order.
+// sequences' order, the heaviest of a sequence first; a warp asks for them in that order, and reads the array on from
+// where it was.
 template <int R>
 struct TileMap {
     const int32_t* cu;
     int nseq, T;
-    int b, e, t;         // up to 32 sequences: this lane's one, its tiles,
-    int first, first128;  // and the tiles before them, of R and of 128 rows
-    int total;           // tiles
+    int s0;                   // the 32 sequences held, from this one on:
+    int b, e, t;              // this lane's one, its tiles,
+    int first, first128;      // and the tiles before them, of R and of 128 rows
+    int upto, upto128, end;   // tiles up to the 32's end, their last token
+    int total;                // tiles of all
 
     static __device__ __forceinline__ int scan(int x) {  // inclusive
 #pragma unroll
@@ -51,37 +54,54 @@ struct TileMap {
         }
         return x;
     }
-    // The 32 sequences from s0 on, `before` and `before128` tiles into the batch, from token `end` on.  Entries
-    // count as the largest so far, within [0, T]: whatever the array holds, the sequences do not overlap, and their
-    // tiles stay within the host's bound.
-    __device__ __forceinline__ void load(int s0, int& before, int& before128, int& end) {
-        const int s = s0 + (int)(threadIdx.x & 31);
-        b = max(s < nseq ? min(__ldg(cu + s), T) : 0, end);
+    // Entry `i` of the array, within [0, T].
+    __device__ __forceinline__ int at(int i) const { return i <= nseq ? min(max(__ldg(cu + i), 0), T) : 0; }
+    // Takes the next 32 sequences, this lane's from entry x to entry y.  Entries count as the largest so far: whatever
+    // the array holds, the sequences do not overlap, and their tiles stay within the host's bound.
+    __device__ __forceinline__ void load(int x, int y) {
+        b = max(x, end);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, b, o);
-            if ((int)(threadIdx.x & 31) >= o) b = max(b, y);
+            const int z = __shfl_up_sync(0xffffffffu, b, o);
+            if ((int)(threadIdx.x & 31) >= o) b = max(b, z);
         }
-        e = max(s < nseq ? min(__ldg(cu + s + 1), T) : 0, b);
+        e = max(y, b);
         end = __shfl_sync(0xffffffffu, e, 31);
         t = (e - b + R - 1) / R;
         int incl = scan(t);
-        first = before + incl - t;
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        first = upto + incl - t;
+        upto += __shfl_sync(0xffffffffu, incl, 31);
         if (R == kRows) {
             first128 = first;
-            before128 = before;
+            upto128 = upto;
         } else {
             const int t128 = (e - b + kRows - 1) / kRows;
             incl = scan(t128);
-            first128 = before128 + incl - t128;
-            before128 += __shfl_sync(0xffffffffu, incl, 31);
+            first128 = upto128 + incl - t128;
+            upto128 += __shfl_sync(0xffffffffu, incl, 31);
         }
     }
     __device__ __forceinline__ TileMap(const int32_t* cu_, int nseq_, int T_) : cu(cu_), nseq(nseq_), T(T_) {
-        int before = 0, before128 = 0, end = 0;
-        for (int s0 = 0; s0 < nseq; s0 += 32) load(s0, before, before128, end);
-        total = before;
+        const int lane = threadIdx.x & 31;
+        s0 = upto = upto128 = end = 0;
+        int x = at(lane), y = at(lane + 1);
+        load(x, y);
+        if (nseq > 32) {
+            const int x0 = x, y0 = y;
+            x = at(lane + 32);
+            y = at(lane + 33);
+            for (int s = 32; s < nseq; s += 32) {
+                const int xn = at(s + lane + 32), yn = at(s + lane + 33);  // on their way during the sums
+                load(x, y);
+                x = xn;
+                y = yn;
+            }
+            total = upto;
+            upto = upto128 = end = 0;
+            load(x0, y0);
+        } else {
+            total = upto;
+        }
     }
     __device__ __forceinline__ void take(Seq& out, int src, int local) const {
         out.begin = __shfl_sync(0xffffffffu, b, src);
@@ -110,17 +130,16 @@ struct TileMap {
             take(out, src, up ? lo - 1 : n - lo);
             return true;
         }
-        const int g = up ? total - 1 - rank : rank;
-        int before = 0, before128 = 0, end = 0;
-        for (int s0 = 0;; s0 += 32) {
-            load(s0, before, before128, end);
-            const uint32_t hit = __ballot_sync(0xffffffffu, g >= first && g < first + t);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                take(out, src, g - __shfl_sync(0xffffffffu, first, src));
-                return true;
-            }
+        while (rank >= upto && s0 < nseq) {
+            s0 += 32;
+            load(at(s0 + lane), at(s0 + lane + 1));
         }
+        const uint32_t hit = __ballot_sync(0xffffffffu, rank >= first && rank < first + t);
+        if (!hit) return false;  // an array that changes meanwhile
+        const int src = __ffs(hit) - 1;
+        const int n = __shfl_sync(0xffffffffu, t, src), i = rank - __shfl_sync(0xffffffffu, first, src);
+        take(out, src, up ? n - 1 - i : i);
+        return true;
     }
 };
 
@@ -189,11 +208,11 @@ struct UnitQueue {
             if (lead && counter) u = (own ? (int64_t)gridDim.x : 0) + atomicAdd(counter, 1);
         }
         u = __shfl_sync(0xffffffffu, u, 0);
-        const bool have = u < (int64_t)map.total * heads;  // below 2^31: the host checks
+        bool have = u < (int64_t)map.total * heads;  // below 2^31: the host checks
         if (have) {
-            Seq sq;
+            Seq sq{};
             const uint32_t rank = (uint32_t)u / (uint32_t)heads;
-            map.find((int)rank, up, sq);
+            have = map.find((int)rank, up, sq);
             x = Unit{sq.begin, sq.len, sq.tile, sq.local, (int)((uint32_t)u - rank * (uint32_t)heads)};
         }
         if (lead) {

@@ -75,6 +75,8 @@ def test_training_step_of_a_layer(lens, Hq, Hk, d, window, rot, il):
     ([131, 1, 0, 7] * 10 + [400], 12, 4, 64, 0),                 # more than 32 sequences; one tile and two
     ([131, 1, 0, 7] * 10 + [400], 9, 3, 64, 50),                 # an odd group: pairs of tiles, the second often missing
     ([20] * 300, 3, 1, 64, 0),
+    ([2] * 500 + [150] + [0, 1] * 40 + [129], 4, 2, 64, 0),      # many runs of 32 sequences, some of them empty
+    ([0] * 70 + [5] + [0] * 70, 2, 1, 128, 0),
     ([1100], 10, 2, 128, 0),
     ([1100, 900], 7, 7, 128, 300),
 ])
