@@ -10,6 +10,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,6 +20,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SELFTEST_LIB = os.path.join(PKG, "libgdn_selftest.so")
+BINDING = os.path.join(PKG, "_attn_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -53,9 +55,33 @@ def up_to_date(lib, srcs) -> bool:
 
 
 def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
-    """Build libgdn.so and the test-only libgdn_selftest.so; returns the libgdn.so path."""
+    """Build libgdn.so, the binding's native module and the test-only libgdn_selftest.so; returns the libgdn.so path."""
     _build_lib(SELFTEST_LIB, selftest_sources(), "selftest_", force, verbose, jobs)
-    return _build_lib(LIB, sources(), "", force, verbose, jobs)
+    _build_lib(LIB, sources(), "", force, verbose, jobs)
+    _build_binding(force, verbose)
+    return LIB
+
+
+def _build_binding(force, verbose):
+    """The native marshalling of the attention layer's short calls, against torch's headers and libgdn.so."""
+    src = os.path.join(CSRC, "binding", "attn_calls.cpp")
+    if not force and up_to_date(BINDING, [src]):
+        return
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", tmp, "-I", INCLUDE, "-isystem", inc,
+           "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+           "-I", sysconfig.get_paths()["include"], "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", PKG, "-l:libgdn.so", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def _build_lib(lib, srcs, prefix, force, verbose, jobs):

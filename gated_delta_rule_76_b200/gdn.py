@@ -623,9 +623,14 @@ def gdn_layer_core_bwd(xq, xk, xv, conv_w, alpha, z, grad_y, b=None, w=None, bet
 # ---------------------------------------------------------------------------------------------
 # the softmax-attention layer of hybrid stacks
 #
-# Serving calls these once a token and layer, on kernels of a few microseconds: the marshalling below
-# keeps to plain comparisons, and builds its structs from positional values.
+# Serving calls these once a token and layer, on kernels of a few microseconds.  They are marshalled natively where
+# their arguments are plain (csrc/binding/attn_calls.cpp: 5 to 8 us a call instead of 13 to 17); the marshalling below
+# takes every other case.
 # ---------------------------------------------------------------------------------------------
+try:
+    from . import _attn_calls as _native
+except ImportError:  # not built: everything goes the general way
+    _native = None
 _AS_IS = contextlib.nullcontext()
 # what torch.cuda.current_device and current_stream come down to once CUDA is up, as it is where a CUDA tensor exists
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -738,6 +743,10 @@ def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, 
                          q_out=None, k_out=None, stream=None):
     """Per-head RMS norm of q [T,Hq,d] and k [T,Hk,d] (or None) and the rotation of their first
     ``2 * len(inv_freq)`` channels by ``positions`` [T] int32.  Returns (q_out, k_out)."""
+    if stream is None and q_out is None and k_out is None and _native is not None:
+        r = _native.qk_norm_rope_fwd(q, k, positions, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
+        if r is not None:
+            return r if type(r) is tuple else check(r, "gdn_qk_norm_rope_fwd")
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, strides = _qk_inputs(q, k)
         q_out, pqo = _result("q_out", q_out, q, dtype, dev)
@@ -757,6 +766,11 @@ def gdn_qk_norm_rope_bwd(q, k, positions=None, inv_freq=None, *, grad_q, grad_k=
                          workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
     """Reverse mode of gdn_qk_norm_rope_fwd for the gradients ``grad_q``, ``grad_k`` of its results.
     Returns dq, dk in the inputs' dtype and dq_norm_w, dk_norm_w [d] fp32 (those that apply)."""
+    if stream is None and workspace is None and _native is not None:
+        r = _native.qk_norm_rope_bwd(q, k, positions, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale, grad_q, grad_k)
+        if r is not None:
+            names = ("dq", "dk", "dq_norm_w", "dk_norm_w")
+            return {n: t for n, t in zip(names, r) if t is not None} if type(r) is tuple else check(r, "gdn_qk_norm_rope_bwd")
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, strides = _qk_inputs(q, k)
         out = {"dq": _result("dq", None, q, dtype, dev)[0]}
@@ -802,6 +816,10 @@ def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: 
     [nseq + 1] (int32 on the device, or a list or CPU tensor, which is checked).  ``scale``: d ** -0.5
     unless given; ``window``: 0, or how many tokens, itself included, a token sees.  Returns o; rows
     outside every sequence stay as they were (unset in an ``o`` made here)."""
+    if stream is None and o is None and workspace is None and _native is not None:
+        r = _native.attn_fwd(q, k, v, cu_seqlens, scale, window, bwd_cache)
+        if r is not None:
+            return r if type(r) is not int else check(r, "gdn_attn_fwd")
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, pv, strides = _qkv(q, k, v)
         pcu, nseq, cu = _cu_seqlens(cu_seqlens, dev, T)
@@ -822,6 +840,10 @@ def gdn_attn_bwd(q, k, v, cu_seqlens, o, *, grad_o, fwd_cache: torch.Tensor, sca
                  stream=None) -> Dict[str, torch.Tensor]:
     """Reverse mode of gdn_attn_fwd from its output ``o`` and the cache it filled.  Returns dq, dk, dv
     in bf16 (``dq``, ``dk``, ``dv``: buffers to fill; rows outside every sequence stay as they were)."""
+    if stream is None and dq is None and dk is None and dv is None and workspace is None and _native is not None:
+        r = _native.attn_bwd(q, k, v, cu_seqlens, scale, window, o, grad_o, fwd_cache)
+        if r is not None:
+            return dict(zip(("dq", "dk", "dv"), r)) if type(r) is tuple else check(r, "gdn_attn_bwd")
     with _on(q, stream):
         dev, dtype, T, Hq, Hk, d, pq, pk, pv, strides = _qkv(q, k, v)
         pcu, nseq, cu = _cu_seqlens(cu_seqlens, dev, T)
@@ -860,6 +882,11 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, context_lens, *, cu_seqle
     before (unchanged); ``cu_seqlens``: the sequences' new tokens, None for one each.  With ``q``
     [T,Hq,d], the same norm and rotation of q.  Returns (q_out or None, k_out or None: the keys as
     cached, with ``want_k``)."""
+    if stream is None and q_out is None and k_out is None and _native is not None:
+        r = _native.kv_append(k, v, k_cache, v_cache, block_table, context_lens, cu_seqlens, q, inv_freq, q_norm_w, k_norm_w,
+                              norm_eps, interleaved, rot_scale, want_k)
+        if r is not None:
+            return r if type(r) is tuple else check(r, "gdn_kv_append")
     with _on(k, stream):
         dev, dtype, T, Hk, d, sk = _first("k", k)
         Hv, sv = _packed("v", v, T, d, dtype, dev)
@@ -888,6 +915,10 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, context_lens, *, scale: Op
     """One query token for N sequences, q [N,Hq,d], over the paged caches: ``context_lens`` [N] int32
     tokens each, this one's included.  ``max_context``: a bound on the lengths that the caller knows
     (0: the block table's reach).  Returns o [N,Hq,d]."""
+    if stream is None and o is None and workspace is None and _native is not None:
+        r = _native.attn_decode(q, k_cache, v_cache, block_table, context_lens, scale, window, max_context)
+        if r is not None:
+            return r if type(r) is not int else check(r, "gdn_attn_decode")
     with _on(q, stream):
         dev, dtype, N, Hq, d, sq = _first("q", q)
         Hk = k_cache.shape[2] if k_cache.dim() == 4 else 0

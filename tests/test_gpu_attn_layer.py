@@ -199,3 +199,92 @@ def test_decode_and_append_in_one_graph_replayed():
         graph.replay()
         assert torch.equal(o, want[i]), i
     assert torch.equal(ctx, ctx1) and torch.equal(kc, kc1) and torch.equal(vc, vc1)
+
+
+def calls():
+    """Every natively marshalled call, with and without its optional arguments: name -> call."""
+    T, Hq, Hk, d, page = 70, 4, 2, 64, 16
+    q, k, v = (rnd(T, h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk)))
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    pos, cu, freq, w = i32(list(range(T))), i32([0, 3, 70]), rnd(16, seed=7, dtype=torch.float32).abs(), rnd(d, seed=8)
+    kc, vc = rnd(12, page, Hk, d, seed=5), rnd(12, page, Hk, d, seed=6)
+    table, ctx = torch.arange(12, dtype=torch.int32, device="cuda").view(2, 6), i32([20, 1])
+    norm = dict(q_norm_w=w, k_norm_w=w, norm_eps=1e-5, interleaved=True, rot_scale=0.5)
+
+    def append(**kw):
+        caches = kc.clone(), vc.clone()
+        return [*gdn.gdn_kv_append(k, v, *caches, table, ctx, cu_seqlens=cu, **kw), *caches]
+
+    def train(**kw):
+        cache = cache_of(q, k, v, cu)
+        cache.zero_()
+        o = gdn.gdn_attn_fwd(q, k, v, cu, bwd_cache=cache, **kw)
+        return [o, cache, *gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=-q, fwd_cache=cache, **kw).values()]
+
+    one = lambda t: t[:2].contiguous()
+    return {
+        "qk grads": lambda: list(gdn.gdn_qk_norm_rope_bwd(q, k, pos, freq, grad_q=-q, grad_k=-k, **norm).values()),
+        "qk grads, q alone": lambda: list(gdn.gdn_qk_norm_rope_bwd(q, None, pos, freq, grad_q=-q).values()),
+        "train": train,
+        "train window": lambda: train(scale=0.3, window=5),
+        "qk": lambda: gdn.gdn_qk_norm_rope_fwd(q, k, pos, freq, **norm),
+        "qk f32, q alone": lambda: gdn.gdn_qk_norm_rope_fwd(q.float(), None, q_norm_w=w.float()),
+        "attn": lambda: [gdn.gdn_attn_fwd(q, k, v, cu)],
+        "attn window": lambda: [gdn.gdn_attn_fwd(q, k, v, cu, scale=0.3, window=5)],
+        "append": lambda: append(q=q, inv_freq=freq, want_k=True, **norm),
+        "append k": lambda: append(inv_freq=freq),
+        "append one": lambda: gdn.gdn_kv_append(one(k), one(v), kc.clone(), vc.clone(), table, ctx, q=one(q)),
+        "decode": lambda: [gdn.gdn_attn_decode(one(q), kc, vc, table, ctx)],
+        "decode window": lambda: [gdn.gdn_attn_decode(one(q), kc, vc, table, ctx, scale=0.2, window=7, max_context=50)],
+    }
+
+
+def test_native_marshalling_is_the_general_one(monkeypatch):
+    assert gdn._native is not None, "the native module is not built"
+    got = {name: f() for name, f in calls().items()}
+    monkeypatch.setattr(gdn, "_native", None)
+    for name, f in calls().items():
+        want = f()
+        assert len(want) == len(got[name])
+        for a, b in zip(got[name], want):
+            assert (a is None and b is None) or torch.equal(a, b), name
+
+
+def test_refusals_say_the_same_through_both(monkeypatch):
+    q, k = rnd(8, 4, 64), rnd(8, 3, 64)
+    cu = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    kc, table, ctx = rnd(4, 16, 2, 64), torch.zeros(8, 2, dtype=torch.int32, device="cuda"), cu[1:].repeat(8)
+    bad = [
+        lambda: gdn.gdn_attn_fwd(q, k, k, cu),                                  # 4 heads on 3
+        lambda: gdn.gdn_attn_fwd(q, q, q, cu, scale=-1.0),
+        lambda: gdn.gdn_attn_fwd(q, q, q, cu, window=-1),
+        lambda: gdn.gdn_attn_fwd(q, q, q.float(), cu),
+        lambda: gdn.gdn_attn_fwd(q, q, q[:4], cu),
+        lambda: gdn.gdn_attn_fwd(q, q, q, cu.long()),
+        lambda: gdn.gdn_attn_fwd(q.float(), q.float(), q.float(), cu),          # bf16 only
+        lambda: gdn.gdn_qk_norm_rope_fwd(q, k, None, torch.ones(8, device="cuda")),
+        lambda: gdn.gdn_qk_norm_rope_fwd(q, k, norm_eps=-1.0),
+        lambda: gdn.gdn_qk_norm_rope_fwd(q, k, q_norm_w=rnd(32)),
+        lambda: gdn.gdn_qk_norm_rope_fwd(rnd(8, 4, 32), None),
+        lambda: gdn.gdn_kv_append(q, q, kc, kc, table, ctx),                    # 4 heads into a cache of 2
+        lambda: gdn.gdn_kv_append(q[:, :2].contiguous(), q[:, :2].contiguous(), kc, kc, table, ctx),  # one cache for both
+        lambda: gdn.gdn_attn_decode(q, kc, kc, table[:4], ctx),
+        lambda: gdn.gdn_attn_decode(q, kc, kc, table, ctx, max_context=-1),
+        lambda: gdn.gdn_attn_decode(q, kc.float(), kc, table, ctx),
+        lambda: gdn.gdn_qk_norm_rope_bwd(q, k, grad_q=q),                       # k without its gradient
+        lambda: gdn.gdn_qk_norm_rope_bwd(q, k, grad_q=q, grad_k=k[:4]),
+        lambda: gdn.gdn_attn_fwd(q, q, q, cu, bwd_cache=torch.empty(256, dtype=torch.uint8, device="cuda")),
+        lambda: gdn.gdn_attn_bwd(q, q, q, cu, q, grad_o=q, fwd_cache=torch.empty(256, dtype=torch.uint8, device="cuda")),
+        lambda: gdn.gdn_attn_bwd(q, q, q, cu, q, grad_o=q[:4], fwd_cache=cache_of(q, q, q, cu)),
+    ]
+
+    def says(f):
+        before = gdn.kernel_launches()
+        with pytest.raises(gdn.GdnError) as e:
+            f()
+        assert gdn.kernel_launches() == before
+        return str(e.value)
+
+    got = [says(f) for f in bad]
+    monkeypatch.setattr(gdn, "_native", None)
+    assert got == [says(f) for f in bad]
