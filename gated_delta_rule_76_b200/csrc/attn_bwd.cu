@@ -709,7 +709,7 @@ cudaError_t attn_bwd(const AttnIO& io, int d, cudaStream_t st) {
     attn::BwdParams p{};
     p.io = io;
     p.tiles = (int)attn_tiles(io.T, io.nseq);
-    p.window = io.window > 0 && io.window < INT32_MAX ? (int)io.window : INT32_MAX;
+    p.window = io.window > 0 && io.window < attn::kNoWindow ? (int)io.window : attn::kNoWindow;
     p.parts = attn_bwd_parts(io.T, io.nseq, io.Hq, io.Hk, io.window);
     p.scale_log2 = io.scale * 1.4426950408889634f;
     return d == 128 ? attn::launch<128>(maps, p, st) : attn::launch<64>(maps, p, st);

@@ -70,7 +70,7 @@ constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;
 struct FwdParams {
     AttnIO io;
     int tiles;         // bound on the 128-row tiles
-    int window;        // INT_MAX: none
+    int window;        // kNoWindow: none
     float scale_log2;
 };
 
@@ -431,7 +431,7 @@ cudaError_t attn_fwd(const AttnIO& io, int d, cudaStream_t st) {
     attn::FwdParams p{};
     p.io = io;
     p.tiles = (int)attn_tiles(io.T, io.nseq);
-    p.window = io.window > 0 && io.window < INT32_MAX ? (int)io.window : INT32_MAX;
+    p.window = io.window > 0 && io.window < attn::kNoWindow ? (int)io.window : attn::kNoWindow;
     p.scale_log2 = io.scale * 1.4426950408889634f;
     if (d == 128) return io.lse ? attn::launch_s<128, true>(maps, p, st) : attn::launch_s<128, false>(maps, p, st);
     return io.lse ? attn::launch_s<64, true>(maps, p, st) : attn::launch_s<64, false>(maps, p, st);

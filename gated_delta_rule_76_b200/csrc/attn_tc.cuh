@@ -24,6 +24,7 @@ using namespace gdn::tc;
 
 constexpr uint64_t kWaitNs = 4000000000ull;
 constexpr int kRows = 128;
+constexpr int kNoWindow = 1 << 30;  // more than any sequence has; differences with it stay within 32 bits
 
 struct Seq {
     int begin, len;   // first token, tokens
