@@ -60,8 +60,11 @@ enum FwdBar {
     B_O = B_PB + 2,       // [2] the unit's last P V done
     B_U = B_O + 2,        // UnitQueue
     B_R = B_U + UnitQueue::kBars,  // [stages] landed
-    B_R_FREE = B_R + 10,  // [4] ring tiles 2q + 1 and 2q + 2 read for the last time (q mod 4)
-    B_COUNT = B_R_FREE + 4
+    // [8] ring tiles 2q + 1 and 2q + 2 read for the last time (q mod 8).  A barrier must not complete again before the
+    // copying warp has waited for it: with 10 stages tile 2q + 10 is loaded once pair q - 1 is free, so that pairs
+    // q to q + 4 may be freed in a row.
+    B_R_FREE = B_R + 10,
+    B_COUNT = B_R_FREE + 8
 };
 static_assert(B_COUNT * 8 <= 304, "barriers");
 // tensor memory: S of either tile, O of either tile
@@ -203,7 +206,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     auto load = [&](const CUtensorMap* map_, int kt) -> bool {
                         if (ri >= NS) {  // the slot's last tile, ri - NS, is free with its pair
                             const int q = ri > NS ? (ri - NS - 1) >> 1 : 0;
-                            if (!wait_bar(cx, B_R_FREE + (q & 3), (q >> 2) & 1)) return false;
+                            if (!wait_bar(cx, B_R_FREE + (q & 7), (q >> 3) & 1)) return false;
                         }
                         uint64_t* bar = cx.bars + B_R + ri % NS;
                         mbar_arrive_expect_tx(bar, L::kTile);
@@ -246,7 +249,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     if (ok) {
                         if (pr.top <= pr.a.hi) s_product<D, 0>(cx, tbase, q_desc, ring_k, at.slot);
                         if (pr.b.hi >= pr.b.lo) s_product<D, 1>(cx, tbase, q_desc, ring_k, at.slot);
-                        if (!first) mma_commit(cx.bars + B_R_FREE + (pairs++ & 3));
+                        if (!first) mma_commit(cx.bars + B_R_FREE + (pairs++ & 7));
                         first = false;
                         if (pr.top == pr.bottom) mma_commit(cx.bars + B_Q_FREE);
                     }
@@ -258,7 +261,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         ok = tile_step<D, 0>(cx, tbase, pr.a, kt, q_desc, ring_k, ring_mn, v, at, p0) &&
                              tile_step<D, 1>(cx, tbase, pr.b, kt, q_desc, ring_k, ring_mn, v, at, p1);
                         if (ok && kt > pr.bottom) {
-                            mma_commit(cx.bars + B_R_FREE + (pairs++ & 3));
+                            mma_commit(cx.bars + B_R_FREE + (pairs++ & 7));
                             if (kt - 1 == pr.bottom) mma_commit(cx.bars + B_Q_FREE);
                         }
                     }

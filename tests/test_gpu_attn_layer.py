@@ -77,6 +77,11 @@ def test_training_step_of_a_layer(lens, Hq, Hk, d, window, rot, il):
     ([20] * 300, 3, 1, 64, 0),
     ([2] * 500 + [150] + [0, 1] * 40 + [129], 4, 2, 64, 0),      # many runs of 32 sequences, some of them empty
     ([0] * 70 + [5] + [0] * 70, 2, 1, 128, 0),
+    # few key tiles: the backward takes them in parts
+    ([1800], 2, 1, 128, 0),
+    ([1793, 3, 900], 3, 3, 64, 0),                                # pairs of tiles of unequal reach
+    ([1500, 640], 1, 1, 128, 700),                                # parts that end at the window's edge
+    ([2050], 5, 1, 64, 1100),
     ([1100], 10, 2, 128, 0),
     ([1100, 900], 7, 7, 128, 300),
 ])
@@ -90,6 +95,26 @@ def test_many_units_a_cta(lens, Hq, Hk, d, window):
     ref.within(o, want, bound, "o")
     for name, x, b in zip(("dq", "dk", "dv"), grads, bounds):
         ref.within(g[name], x, b, name)
+
+
+def test_short_units_in_a_row_keep_the_copies_in_step():
+    """Many units of one or two key tiles at heads of 64, whose ring of key tiles runs five pairs ahead: no wait may
+    expire, and every run gives the same bits."""
+    lens = [1, 1, 0, 128, 0, 64, 63, 64, 1, 200, 2, 65, 64, 1, 2, 2, 64, 129, 2, 64, 64, 128, 65, 128, 128, 1, 0, 64, 127, 65, 127,
+            63, 64, 1, 64, 129, 63, 200, 127, 0, 63, 0, 127, 2]
+    st = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for Hq, Hk, d, window in ((24, 8, 64, 1), (24, 8, 64, 0), (16, 8, 64, 1), (16, 8, 128, 1)):
+        T, cu = sum(lens), torch.tensor(starts(lens), dtype=torch.int32, device="cuda")
+        q, k, v = (rnd(T, h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk)))
+        want, bound = ref.packed(q, k, v, starts(lens), d ** -0.5, window)
+        ws = torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+        first = None
+        for _ in range(30):
+            o = gdn.gdn_attn_fwd(q, k, v, cu, window=window, workspace=ws)
+            assert gdn.load().gdn_workspace_status(ctypes.c_void_p(ws.data_ptr()), st) == 0
+            first = o if first is None else first
+            assert torch.equal(o, first)
+        ref.within(first, want, bound, "o")
 
 
 def test_calls_on_two_streams_at_once():
