@@ -94,15 +94,16 @@ inline int64_t attn_tiles(int64_t T, int64_t nseq) { return T / 128 + (nseq < T 
 // Parts that dkdv cuts a key tile's unit into.  The heaviest unit, the first key tile of a sequence with all the
 // group's queries, takes as long as the SMs' average of dkdv's and dq's work together at 160 units (one sequence or
 // several equal ones), or at 80 where a window makes the units alike; with fewer it would be what the call waits for
-// (backward of 4096 tokens, 16 heads on 2: 515 us whole, 258 us in 3 parts; one sequence of 2600, 8 heads on 1: 344 and
-// 112 us).  A part costs its sums' way through memory (2600 tokens, 16 heads on 4, window 500, 88 units: 67 us whole,
-// 79 us in 3 parts).
+// (backward of 4096 tokens, 16 heads on 2: 515 us whole, 247 us in 3 parts; one sequence of 2600, 8 heads on 1: 344 and
+// 86 us).  A part costs its sums' way through memory (4 x 2048 tokens, 16 heads on 4, 272 units: 266 us whole, 314 us in 2
+// parts), and is worth it from two items on.
 inline int attn_bwd_parts(int64_t T, int64_t nseq, int64_t Hq, int64_t Hk, int64_t window) {
     const int64_t units = attn_tiles(T, nseq) * Hk, items = Hq / Hk * ((T + 127) / 128);
     const int64_t want = window > 0 && window < T / 2 ? 80 : 192;
     int64_t parts = (want + units - 1) / units;
     if (parts > 16) parts = 16;
-    return (int)(parts < items ? parts : items);
+    if (parts > items / 2) parts = items / 2;
+    return parts < 1 ? 1 : (int)parts;
 }
 cudaError_t attn_fwd(const AttnIO& io, int d, cudaStream_t st);
 cudaError_t attn_bwd(const AttnIO& io, int d, cudaStream_t st);

@@ -624,37 +624,37 @@ __global__ void __launch_bounds__(256) attn_delta_kernel(const AttnIO io, int ti
     }
 }
 
-// dk and dv of a key tile and head from the parts' sums, in their order.  D / 4 lanes a row, 32 rows a block.
+// dk and dv of a key tile and head from the parts' sums, in their order.  D / 4 lanes a row, a row a lane.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const BwdParams p) {
-    constexpr int LANES = D / 4, RPP = 256 / LANES;
-    grid_wait();
+    constexpr int LANES = D / 4;
     Seq sq{};
-    const int hk = blockIdx.x % p.io.Hk;
+    const int hk = blockIdx.x % p.io.Hk, G = p.io.Hq / p.io.Hk;
     TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
-    if (!map.find((int)(blockIdx.x / p.io.Hk), false, sq)) return;
+    const bool have = map.find((int)(blockIdx.x / p.io.Hk), false, sq);
+    const int row = sq.local * kRows + blockIdx.y * (256 / LANES) + threadIdx.x / LANES;
+    grid_wait();
+    if (!have || row >= sq.len) return;
     const Unit un{sq.begin, sq.len, sq.tile, sq.local, hk};
-    const int64_t stride = (int64_t)p.io.Hk * D, all = (int64_t)p.io.T * stride;
-    const int c = (threadIdx.x % LANES) * 4;
-#pragma unroll
-    for (int r = threadIdx.x / LANES; r < 32; r += RPP) {
-        const int row = sq.local * kRows + blockIdx.y * 32 + r;
-        if (row >= sq.len) return;
-        const int64_t at = (sq.begin + row) * stride + hk * D + c;
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        for (int s = 0; s < p.parts; ++s) {
-            if (part_of(un, s, p.parts, p.io.Hq / p.io.Hk, p.window).m == 0) continue;  // nothing was written
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(p.io.part_dk + s * all + at));
-            const float4 b = __ldcg(reinterpret_cast<const float4*>(p.io.part_dv + s * all + at));
-            k.x += a.x; k.y += a.y; k.z += a.z; k.w += a.w;
-            v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
-        }
-        const float f = p.io.scale;
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.dk) + at) =
-            make_uint2(pack_bf16x2(k.x * f, k.y * f), pack_bf16x2(k.z * f, k.w * f));
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.dv) + at) =
-            make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    // with fewer items than parts some are empty, and nothing was written for them
+    const bool all = (int64_t)G * query_tiles(un, p.window) >= p.parts;
+    const int64_t stride = (int64_t)p.io.Hk * D, step = (int64_t)p.io.T * stride;
+    const int64_t at = (sq.begin + row) * stride + hk * D + (threadIdx.x % LANES) * 4;
+    float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+#pragma unroll 4
+    for (int s = 0; s < p.parts; ++s) {
+        const bool there = all || part_of(un, s, p.parts, G, p.window).m;
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 a = there ? __ldcg(reinterpret_cast<const float4*>(p.io.part_dk + s * step + at)) : zero;
+        const float4 b = there ? __ldcg(reinterpret_cast<const float4*>(p.io.part_dv + s * step + at)) : zero;
+        k.x += a.x; k.y += a.y; k.z += a.z; k.w += a.w;
+        v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
     }
+    const float f = p.io.scale;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.dk) + at) =
+        make_uint2(pack_bf16x2(k.x * f, k.y * f), pack_bf16x2(k.z * f, k.w * f));
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.dv) + at) =
+        make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
 template <int D>
@@ -688,7 +688,7 @@ cudaError_t launch(const CUtensorMap* maps, const BwdParams& p, cudaStream_t st)
     e = cudaLaunchKernelEx(&cfg, attn_dq_kernel<D>, maps[0], maps[1], maps[2], maps[3], p);
     count_launch();
     if (e != cudaSuccess || p.parts == 1) return e;
-    cfg.gridDim = dim3(k_tiles, 4);
+    cfg.gridDim = dim3(k_tiles, kRows * (D / 4) / 256);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
     e = cudaLaunchKernelEx(&cfg, attn_join_kernel<D>, p);
