@@ -84,6 +84,9 @@ struct AttnIO {
     const void* grad_o;
     void *dq, *dk, *dv;
     float* delta;              // [Hq][tiles][128]: rows' -sum of grad_o .* o
+    // forward, where units are cut into parts: their sums, and each row's reference and sum of weights
+    float* part_o;             // [parts][T][Hq][d]
+    float2* part_ml;           // [parts][T][Hq]
     float *part_dk, *part_dv;  // [parts][T][Hk][d], where the key tiles' units are cut into parts
     int* err;                  // device error word
     int* counters;             // [2] the units drawn so far (forward and dkdv; dq)
@@ -104,6 +107,29 @@ inline int attn_bwd_parts(int64_t T, int64_t nseq, int64_t Hq, int64_t Hk, int64
     if (parts > 16) parts = 16;
     if (parts > items / 2) parts = items / 2;
     return parts < 1 ? 1 : (int)parts;
+}
+// Parts that the forward cuts a unit's key tiles into, as the least estimate (us).  Where there are few units, the longest
+// row's key tiles, one after the other, are what the call waits for: 2 us a tile, 1.6 with heads of 64.  A part has its own
+// start and end, 5 us, and its sums' way through memory and the joining kernel.  The sequences' lengths are not known
+// here: the longest is taken as twice what is left for one more (8192 tokens, 4 heads on 1: 124 us whole, 84 us in 2 parts;
+// 1783 and 7 tokens, 3 heads: 32 and 25 us; 1777, 16 heads, left whole: 33 us, 47 in 3 parts).
+inline int attn_fwd_parts(int64_t T, int64_t nseq, int64_t Hq, int64_t d, int64_t window) {
+    if (T < 1 || nseq < 1) return 1;
+    const double units = (double)((attn_tiles(T, nseq) * Hq + 1) / 2), sums = (double)(T * Hq * d) * 4.0;
+    int64_t tiles = (2 * T / (nseq + 1) + 127) / 128;
+    if (window > 0 && window / 128 + 2 < tiles) tiles = window / 128 + 2;
+    const double chain = (d == 128 ? 2.0 : 1.6) * (double)tiles;
+    double least = 0.0;
+    int parts = 1;
+    for (int p = 1; p <= 8 && (p == 1 || p * 3 <= tiles); ++p) {
+        const double longest = chain / p + 5.0, even = units * (chain / 2.0 + 5.0 * p) / 148.0;
+        const double t = (longest > even ? longest : even) + (p > 1 ? 4.0 + p * sums / 2.5e6 : 0.0);
+        if (p == 1 || t < 0.95 * least) {
+            least = t;
+            parts = p;
+        }
+    }
+    return parts;
 }
 cudaError_t attn_fwd(const AttnIO& io, int d, cudaStream_t st);
 cudaError_t attn_bwd(const AttnIO& io, int d, cudaStream_t st);

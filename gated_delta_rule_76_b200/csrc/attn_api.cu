@@ -131,6 +131,14 @@ size_t cache_bytes(int64_t T, int64_t nseq, int64_t Hq, int64_t d) {
     return T > 0 && nseq > 0 ? lse_bytes(T, nseq, Hq) + (size_t)(T * Hq * d) * 2 : 0;
 }
 
+// The forward's partial sums (none where a unit is one part): the rows' o, then their references and weights.
+size_t fwd_part_o_bytes(const gdn_attn_fwd_args* a, int parts) {
+    return align256((size_t)parts * (size_t)(a->T * a->Hq * a->d) * sizeof(float));
+}
+size_t fwd_part_bytes(const gdn_attn_fwd_args* a) {
+    const int parts = attn_fwd_parts(a->T, a->nseq, a->Hq, a->d, a->window);
+    return parts > 1 ? fwd_part_o_bytes(a, parts) + align256((size_t)parts * (size_t)(a->T * a->Hq) * sizeof(float2)) : 0;
+}
 // One of the backward's two arrays of partial sums (none where a unit is one part).
 size_t part_bytes(const gdn_attn_bwd_args* a) {
     const int parts = attn_bwd_parts(a->T, a->nseq, a->Hq, a->Hk, a->window);
@@ -250,7 +258,7 @@ size_t gdn_attn_fwd_cache_size(const gdn_attn_fwd_args* a) {
 
 size_t gdn_attn_fwd_workspace_size(const gdn_attn_fwd_args* a) {
     if (!a || a->T < 1 || a->T >= kMaxTokens || a->Hq < 1 || a->Hk < 1 || a->d < 1) return 0;
-    return with_copies(256, attn_copy_bytes(a));
+    return with_copies(256 + fwd_part_bytes(a), attn_copy_bytes(a));
 }
 
 gdn_status gdn_attn_fwd(const gdn_attn_fwd_args* a, void* workspace, size_t workspace_bytes, gdn_stream stream) {
@@ -269,10 +277,13 @@ gdn_status gdn_attn_fwd(const gdn_attn_fwd_args* a, void* workspace, size_t work
     if ((s = check_workspace(workspace, workspace_bytes, gdn_attn_fwd_workspace_size(a)))) return s;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     gdn_attn_fwd_args pa = *a;
-    cudaError_t e = attn_copy(&pa, static_cast<char*>(workspace) + 256, st);
+    char* ws = static_cast<char*>(workspace);
+    cudaError_t e = attn_copy(&pa, ws + 256 + fwd_part_bytes(a), st);
     if (e == cudaSuccess) {
         AttnIO io = attn_io(&pa, workspace);
         io.o = a->o;
+        io.part_o = reinterpret_cast<float*>(ws + 256);
+        io.part_ml = reinterpret_cast<float2*>(ws + 256 + fwd_part_o_bytes(a, attn_fwd_parts(a->T, a->nseq, a->Hq, a->d, a->window)));
         if (a->bwd_cache) cache_into(&io, a->bwd_cache);
         e = attn_fwd(io, (int)a->d, st);
     }

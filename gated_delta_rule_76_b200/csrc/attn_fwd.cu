@@ -25,6 +25,8 @@
 // the two tiles share each copy of K and V), the exponentials as long (16 a cycle and SM).  A prompt of 16384
 // tokens, 8 heads of 128 on one: 440 us, 1250 TFLOP/s, the tensor pipe active 57% of the time.  At a unit's end the CTA
 // waits about 3500 cycles more for the last P V, the rows on their way out and the first masked tile.
+// Where units are few, each is cut into parts of its key tiles (attn.h), whose sums against their own references go through
+// the workspace in fp32 and are joined by a second kernel.
 // Tried and slower: 3 of 8 exponentials by a polynomial on the FMA pipe (514 us instead of 447: the softmax's
 // instructions are in the chain, the exponential unit is not what it waits for); S in steps of 64 keys with two
 // buffers each (636 us: the narrow product takes 386 cycles instead of 256, and every step its own waits); units of one
@@ -74,34 +76,48 @@ struct FwdParams {
     AttnIO io;
     int tiles;         // bound on the 128-row tiles
     int window;        // kNoWindow: none
+    int parts;         // of a unit's key tiles
     float scale_log2;
 };
 
-// The two tiles of a unit: first row within the sequence, query head, and key tiles hi down to lo (hi < lo: the
-// tile does not exist).
+// The two tiles of a unit: first row within the sequence, its own key tile, query head, and key tiles hi down to lo
+// (hi < lo: there is nothing to do, or no such tile).
 struct Tile {
-    int row0, head, hi, lo;
+    int row0, diag, head, hi, lo;
 };
 struct Pair {
     Tile a, b;
-    int top, bottom;  // key tiles of either
+    int top, bottom;  // key tiles of either; top < bottom: none
+    int part;
 };
 template <bool PAIR_HEADS>
-__device__ __forceinline__ Tile tile_of(const Unit& un, int window, int s) {
+__device__ __forceinline__ Tile tile_of(const Unit& un, int unit_head, int window, int s) {
     Tile t;
     t.row0 = PAIR_HEADS ? un.local * kRows : (2 * un.local + s) * kRows;
-    t.head = PAIR_HEADS ? 2 * un.head + s : un.head;
-    t.hi = t.row0 / kRows;
+    t.head = PAIR_HEADS ? 2 * unit_head + s : unit_head;
+    t.diag = t.hi = t.row0 / kRows;
     t.lo = t.row0 < un.len ? max(0, t.row0 - window + 1) / kRows : t.hi + 1;
     return t;
 }
-template <bool PAIR_HEADS>
-__device__ __forceinline__ Pair pair_of(const Unit& un, int window) {
+template <bool PAIR_HEADS, bool PARTS>
+__device__ __forceinline__ Pair pair_of(const Unit& un, const FwdParams& p) {
     Pair pr;
-    pr.a = tile_of<PAIR_HEADS>(un, window, 0);
-    pr.b = tile_of<PAIR_HEADS>(un, window, 1);
+    const int unit_head = PARTS ? un.head / p.parts : un.head;
+    pr.part = un.head - (PARTS ? unit_head * p.parts : un.head);
+    pr.a = tile_of<PAIR_HEADS>(un, unit_head, p.window, 0);
+    pr.b = tile_of<PAIR_HEADS>(un, unit_head, p.window, 1);
     pr.top = pr.b.hi >= pr.b.lo ? pr.b.hi : pr.a.hi;
     pr.bottom = pr.a.lo;  // the first tile exists, and sees at least as far back
+    if (PARTS) {
+        const int64_t n = pr.top - pr.bottom + 1;
+        const int from = (int)(n * pr.part / p.parts), to = (int)(n * (pr.part + 1) / p.parts);
+        pr.bottom = pr.top - to + 1;
+        pr.top -= from;
+        pr.a.hi = min(pr.a.hi, pr.top);
+        pr.b.hi = min(pr.b.hi, pr.top);
+        pr.a.lo = max(pr.a.lo, pr.bottom);
+        pr.b.lo = max(pr.b.lo, pr.bottom);
+    }
     return pr;
 }
 
@@ -155,7 +171,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-template <int D, bool SAVE, bool PAIR_HEADS>
+// PARTS: units are cut into parts of their key tiles (attn.h).
+template <int D, bool SAVE, bool PAIR_HEADS, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -164,7 +181,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     const int tid = threadIdx.x, warp = tid >> 5;
-    const int G = p.io.Hq / p.io.Hk, heads = PAIR_HEADS ? p.io.Hq / 2 : p.io.Hq;
+    const int G = p.io.Hq / p.io.Hk, heads = (PAIR_HEADS ? p.io.Hq / 2 : p.io.Hq) * (PARTS ? p.parts : 1);
 
     Ctx cx;
     cx.bars = reinterpret_cast<uint64_t*>(sm + L::kBar);
@@ -200,7 +217,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             int owns = 0, ri = 0;  // Q loads and ring loads issued
             TileMap<PAIR_HEADS ? kRows : 2 * kRows> map(p.io.cu, p.io.nseq, p.io.T);
             while (units.draw(cx, map, heads, true, p.io.counters, un, ok)) {
-                const Pair pr = pair_of<PAIR_HEADS>(un, p.window);
+                const Pair pr = pair_of<PAIR_HEADS, PARTS>(un, p);
+                if (PARTS && pr.top < pr.bottom) continue;
                 const int hk = pr.a.head / G;
                 if ((tid & 31) == 0) {
                     auto load = [&](const CUtensorMap* map_, int kt) -> bool {
@@ -242,12 +260,13 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             const uint32_t q_desc = desc_k(sb + L::kQ), ring_k = desc_k(sb + L::kRing), ring_mn = desc_mn(sb + L::kRing);
             bool first = true;
             while (units.take(cx, un, ok)) {
-                const Pair pr = pair_of<PAIR_HEADS>(un, p.window);
+                const Pair pr = pair_of<PAIR_HEADS, PARTS>(un, p);
+                if (PARTS && pr.top < pr.bottom) continue;
                 if ((tid & 31) == 0) {
                     ok = wait_bar(cx, B_Q, q_parity) && at.landed(cx);
                     q_parity ^= 1u;
                     if (ok) {
-                        if (pr.top <= pr.a.hi) s_product<D, 0>(cx, tbase, q_desc, ring_k, at.slot);
+                        if (pr.top <= pr.a.hi && (!PARTS || pr.top >= pr.a.lo)) s_product<D, 0>(cx, tbase, q_desc, ring_k, at.slot);
                         if (pr.b.hi >= pr.b.lo) s_product<D, 1>(cx, tbase, q_desc, ring_k, at.slot);
                         if (!first) mma_commit(cx.bars + B_R_FREE + (pairs++ & 7));
                         first = false;
@@ -279,7 +298,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         int gi = 0, done = 0;  // items and units of this tile so far
         int ri = 0;            // ring tiles so far
         while (units.take(cx, un, ok)) {
-            const Pair pr = pair_of<PAIR_HEADS>(un, p.window);
+            const Pair pr = pair_of<PAIR_HEADS, PARTS>(un, p);
             const Tile me = s_ ? pr.b : pr.a;
             const int row0 = me.row0, hi = me.hi, lo = me.lo;
             const int row = row0 + lane;
@@ -293,7 +312,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 tmem_ld_wait();
                 const int key0 = kt * kRows;
                 // keys after the row, or out of its window, leave the softmax
-                if (kt == hi || key0 <= row0 + kRows - 1 - p.window) {
+                if (kt == (PARTS ? me.diag : hi) || key0 <= row0 + kRows - 1 - p.window) {
                     const int last = row - key0;
 #pragma unroll
                     for (int c = 0; c < 4; ++c) mask_columns(s[c], columns(last - p.window + 1 - 32 * c, last - 32 * c), kMinusInf);
@@ -307,7 +326,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                 }
                 const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
                 if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                    const float mn = fmaxf(m, mx), f = kt < hi ? exp2_approx(m - mn) : 0.f;
+                    const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
                     m = mn;
                     l *= f;
                     if (kt < hi) {
@@ -322,7 +341,9 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                         }
                     }
                 }
-                const f2 nm = f2_of(-m, -m);
+                // a row that sees none of the keys so far (in a part that starts at the window's edge) keeps p = 0
+                const float nm1 = PARTS && m == -INFINITY ? 0.f : -m;
+                const f2 nm = f2_of(nm1, nm1);
                 f2 sum[2] = {f2_of(0.f, 0.f), f2_of(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
@@ -338,7 +359,7 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     }
                     tmem_st16(t_s + 16 * c, w);
                     if (c == 1) {
-                        if (kt == hi && un.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
+                        if (kt == (PARTS ? me.diag : hi) && un.len - key0 < kRows && (!PAIR_HEADS || s_ == 0)) {
                             // V's rows past the sequence: p is 0 there, but 0 * NaN is not.  Two heads share the
                             // tile, whose product with P1 follows the one with P0.
                             const int slot = ri + 2 * (pr.top - kt) + 1;
@@ -359,16 +380,27 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             ri += 2 * (pr.top - pr.bottom + 1);
             if (!ok) break;
+            const bool live = row < un.len;
+            if (PARTS && live) p.io.part_ml[((int64_t)pr.part * p.io.T + un.begin + row) * p.io.Hq + me.head] = make_float2(m, l);
             if (hi < lo) continue;
             if (!(ok = wait_warp(cx, B_O + s_, done & 1))) break;
             ++done;
             tc_fence_after();
             // the next unit's first product into O waits for its P, which follows this
-            const bool live = row < un.len;
-            const float inv = 1.f / l;
             const int64_t stride = (int64_t)p.io.Hq * D;
             const int first = row - (lane & 31), rows = un.len - first;  // of the warp
             const int64_t at = (int64_t)(un.begin + first) * stride + me.head * D;
+            if (PARTS) {
+#pragma unroll
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[32];
+                    tmem_ld32(t_o + c, o);
+                    tmem_ld_wait();
+                    store_rows_f32(p.io.part_o + (int64_t)pr.part * p.io.T * stride + at + c, stride, o, rows);
+                }
+                continue;
+            }
+            const float inv = 1.f / l;
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 64) {
                 uint32_t o[2][32];
@@ -401,25 +433,86 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (warp == kMmaWarp) tmem_dealloc(tbase, TM_COLS);
 }
 
-template <int D, bool SAVE, bool PAIR_HEADS>
+// o of a tile of rows and a head from its parts: each has the sums of its keys against its own reference m.
+// D / 4 lanes a row, a row a lane.
+template <int D, bool SAVE>
+__global__ void __launch_bounds__(256) attn_fwd_join_kernel(const FwdParams p) {
+    constexpr int LANES = D / 4;
+    Seq sq{};
+    const int head = blockIdx.x % p.io.Hq;
+    TileMap<kRows> map(p.io.cu, p.io.nseq, p.io.T);
+    const bool have = map.find((int)(blockIdx.x / p.io.Hq), true, sq);
+    const int r = blockIdx.y * (256 / LANES) + threadIdx.x / LANES, row = sq.local * kRows + r, c = (threadIdx.x % LANES) * 4;
+    grid_wait();
+    if (!have) return;
+    float nlse = 0.f;  // of rows past the sequence
+    if (row < sq.len) {
+        const int64_t rows = (int64_t)p.io.T * p.io.Hq, at = (int64_t)(sq.begin + row) * p.io.Hq + head;
+        float m = -INFINITY;
+#pragma unroll 4
+        for (int s = 0; s < p.parts; ++s) m = fmaxf(m, __ldcg(p.io.part_ml + s * rows + at).x);
+        float l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int s = 0; s < p.parts; ++s) {
+            const float2 ml = __ldcg(p.io.part_ml + s * rows + at);
+            const bool sees = ml.x != -INFINITY;  // else nothing was written
+            const float f = sees ? exp2_approx(ml.x - m) : 0.f;
+            const float4 o = sees ? __ldcg(reinterpret_cast<const float4*>(p.io.part_o + (s * rows + at) * D + c))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            l = fmaf(f, ml.y, l);
+            v[0] = fmaf(f, o.x, v[0]);
+            v[1] = fmaf(f, o.y, v[1]);
+            v[2] = fmaf(f, o.z, v[2]);
+            v[3] = fmaf(f, o.w, v[3]);
+        }
+        const float inv = 1.f / l;
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float x = v[2 * i] * inv, y = v[2 * i + 1] * inv;
+            hi[i] = pack_bf16x2(x, y);
+            lo[i] = pack_bf16x2(x - __uint_as_float(hi[i] << 16), y - __uint_as_float(hi[i] & 0xFFFF0000u));
+        }
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.o) + at * D + c) = make_uint2(hi[0], hi[1]);
+        if (SAVE) *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.io.o_lo) + at * D + c) = make_uint2(lo[0], lo[1]);
+        nlse = -(m + log2f(l));
+    }
+    if (SAVE && c == 0) p.io.lse[((int64_t)head * p.tiles + sq.tile) * kRows + r] = nlse;
+}
+
+template <int D, bool SAVE, bool PAIR_HEADS, bool PARTS>
 cudaError_t launch(const CUtensorMap* maps, FwdParams p, cudaStream_t st) {
-    auto kernel = attn_fwd_kernel<D, SAVE, PAIR_HEADS>;
+    auto kernel = attn_fwd_kernel<D, SAVE, PAIR_HEADS, PARTS>;
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FwdSmem<D>::kBytes);
     cudaFuncAttributes attr;
     if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kernel);
     if (e != cudaSuccess) return e;
     if (attr.numRegs < kRegs) return cudaErrorInvalidConfiguration;  // setmaxnreg counts on them
-    const int64_t units = (int64_t)p.tiles * p.io.Hq / (PAIR_HEADS ? 2 : 1);
+    const int64_t units = (int64_t)p.tiles * p.io.Hq / (PAIR_HEADS ? 2 : 1) * p.parts;
     if (units <= 148) p.io.counters = nullptr;  // a unit a CTA
     else if ((e = cudaMemsetAsync(p.io.counters, 0, sizeof(int), st)) != cudaSuccess) return e;
     kernel<<<(unsigned)(units < 148 ? units : 148), kThreads, FwdSmem<D>::kBytes, st>>>(maps[0], maps[1], maps[2], p);
     count_launch();
-    return cudaGetLastError();
+    if ((e = cudaGetLastError()) != cudaSuccess || !PARTS) return e;
+    cudaLaunchAttribute early{};
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)p.tiles * (unsigned)p.io.Hq, kRows * (D / 4) / 256);
+    cfg.blockDim = dim3(256);
+    cfg.stream = st;
+    cfg.attrs = &early;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attn_fwd_join_kernel<D, SAVE>, p);
+    count_launch();
+    return e;
 }
 template <int D, bool SAVE>
 cudaError_t launch_s(const CUtensorMap* maps, const FwdParams& p, cudaStream_t st) {
-    return p.io.Hq / p.io.Hk % 2 == 0 ? launch<D, SAVE, true>(maps, p, st) : launch<D, SAVE, false>(maps, p, st);
+    const bool pairs = p.io.Hq / p.io.Hk % 2 == 0;
+    if (p.parts > 1) return pairs ? launch<D, SAVE, true, true>(maps, p, st) : launch<D, SAVE, false, true>(maps, p, st);
+    return pairs ? launch<D, SAVE, true, false>(maps, p, st) : launch<D, SAVE, false, false>(maps, p, st);
 }
 
 }  // namespace
@@ -434,6 +527,7 @@ cudaError_t attn_fwd(const AttnIO& io, int d, cudaStream_t st) {
     attn::FwdParams p{};
     p.io = io;
     p.tiles = (int)attn_tiles(io.T, io.nseq);
+    p.parts = attn_fwd_parts(io.T, io.nseq, io.Hq, d, io.window);
     p.window = io.window > 0 && io.window < attn::kNoWindow ? (int)io.window : attn::kNoWindow;
     p.scale_log2 = io.scale * 1.4426950408889634f;
     if (d == 128) return io.lse ? attn::launch_s<128, true>(maps, p, st) : attn::launch_s<128, false>(maps, p, st);

@@ -358,16 +358,9 @@ __device__ __forceinline__ void arrive_warp(const Ctx& cx, int bar) {
     if ((threadIdx.x & 31) == 0) mbar_arrive(cx.bars + bar);
 }
 
-// 32 columns of 32 consecutive rows, a row a lane, as bf16 to dst (the first lane's row; rows `stride` elements apart),
-// for the rows below `rows`.  Four lanes exchange their 16-byte pieces first, so that a store writes 64 bytes each of
-// 8 rows: a store of 16 bytes each of 32 rows takes the load/store unit 32 cycles, which the whole CTA waits for at
-// the end of its unit of work.  All lanes.
-__device__ __forceinline__ void store_rows(__nv_bfloat16* dst, int64_t stride, const float (&x)[32], int rows) {
+// Four lanes' 16-byte pieces exchanged, w[lane][piece] for w[piece][lane]: rows and columns 1 apart, then 2.  All lanes.
+__device__ __forceinline__ void exchange4(uint32_t (&w)[4][4]) {
     const int lane = threadIdx.x & 31;
-    uint32_t w[4][4];  // piece, word
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
-    // transposes the four lanes' pieces: rows and columns 1 apart, then 2
 #pragma unroll
     for (int o = 1; o <= 2; ++o) {
         const bool odd = lane & o;
@@ -382,11 +375,38 @@ __device__ __forceinline__ void store_rows(__nv_bfloat16* dst, int64_t stride, c
             }
         }
     }
+}
+// 32 columns of 32 consecutive rows, a row a lane, as bf16 to dst (the first lane's row; rows `stride` elements apart),
+// for the rows below `rows`.  Four lanes exchange their 16-byte pieces first, so that a store writes 64 bytes each of
+// 8 rows: a store of 16 bytes each of 32 rows takes the load/store unit 32 cycles, which the whole CTA waits for at
+// the end of its unit of work.  All lanes.
+__device__ __forceinline__ void store_rows(__nv_bfloat16* dst, int64_t stride, const float (&x)[32], int rows) {
+    const int lane = threadIdx.x & 31;
+    uint32_t w[4][4];  // piece, word
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    exchange4(w);
     dst += (lane & ~3) * stride + 8 * (lane & 3);
     rows -= lane & ~3;
 #pragma unroll
     for (int i = 0; i < 4; ++i, dst += stride)
         if (i < rows) *reinterpret_cast<uint4*>(dst) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+}
+// The same of 32 columns as they are, fp32.
+__device__ __forceinline__ void store_rows_f32(float* dst, int64_t stride, const uint32_t (&x)[32], int rows) {
+    const int lane = threadIdx.x & 31;
+    dst += (lane & ~3) * stride + 4 * (lane & 3);
+    rows -= lane & ~3;
+#pragma unroll
+    for (int c = 0; c < 32; c += 16) {
+        uint32_t w[4][4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = x[c + i];
+        exchange4(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < rows) *reinterpret_cast<uint4*>(dst + i * stride + c) = make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
+    }
 }
 
 }  // namespace attn
