@@ -90,7 +90,6 @@ struct AttnIO {
     float *part_dk, *part_dv;  // [parts][T][Hk][d], where the key tiles' units are cut into parts
     int* err;                  // device error word
     int* counters;             // [2] the units drawn so far (forward and dkdv; dq)
-    uint64_t wait_ns;          // limit of one bounded wait, 0: the default
 };
 // Tiles of 128 rows over all sequences, at most.
 inline int64_t attn_tiles(int64_t T, int64_t nseq) { return T / 128 + (nseq < T ? nseq : T); }

@@ -88,7 +88,6 @@ __device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const
     tmem_slot = reinterpret_cast<uint32_t*>(bars + 224);
     cx.abort_flag = reinterpret_cast<volatile int*>(bars + 228);
     cx.err = io.err;
-    cx.wait_ns = io.wait_ns ? io.wait_ns : kWaitNs;
     if (smem_u32(sm) & 1023u) {
         if (threadIdx.x == 0) atomicOr(cx.err, 1);
         return false;
@@ -112,11 +111,11 @@ __device__ __forceinline__ bool setup(Ctx& cx, uint8_t* sm, uint8_t* bars, const
 // many of each were issued.
 __device__ __forceinline__ void drain(const Ctx& cx, int owns, int a_items, int b_items) {
     if (!*cx.abort_flag) return;
-    if (owns) mbar_wait(cx.bars + B_OWN, (owns - 1) & 1, cx.wait_ns);
+    if (owns) mbar_wait(cx.bars + B_OWN, (owns - 1) & 1, kWaitNs);
     for (int i = a_items < 3 ? 0 : a_items - 3; i < a_items; ++i)
-        mbar_wait(cx.bars + B_A + i % 3, (i / 3) & 1, cx.wait_ns);
+        mbar_wait(cx.bars + B_A + i % 3, (i / 3) & 1, kWaitNs);
     for (int i = b_items < 2 ? 0 : b_items - 2; i < b_items; ++i)
-        mbar_wait(cx.bars + B_B + (i & 1), (i >> 1) & 1, cx.wait_ns);
+        mbar_wait(cx.bars + B_B + (i & 1), (i >> 1) & 1, kWaitNs);
 }
 
 // D (+)= A B with A [128 x 128] bf16 in tensor memory as two halves of 32 columns, 64 columns apart, and

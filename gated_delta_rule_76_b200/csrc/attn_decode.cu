@@ -18,7 +18,7 @@
 // combine_kernel, both in index order, so results do not depend on timing.
 //
 // Measured, d = 128: 256 sequences of 64 to 4500 tokens, 16 heads on 2: 58.6 us, 4.7 TB/s (a copy: 6.5); one sequence of 8191
-// tokens: 10 us, two kernels' latency (8.4 MB would take 1.3).
+// tokens: 8.7 us, two kernels' latency (8.4 MB would take 1.3).
 #include <cuda_bf16.h>
 
 #include "attn.h"
@@ -455,15 +455,18 @@ cudaError_t launch_d(DecodeAttnParams p, cudaStream_t st) {
 }  // namespace
 
 // Chunk length and number of chunks for contexts of up to `reach` tokens (and the tile before a window's
-// start).  Eight CTAs' worth of work an SM evens out ragged lengths, chunks of at most 512 tokens keep a long
+// start).  Eight CTAs' worth of work an SM evens out ragged lengths; chunks of at most 512 tokens keep a long
 // sequence from being the tail (256 sequences of 64 to 4500 tokens: 58.6 us; 59.1 us with 1024, 78 us with 256, whose
-// joins cost more), and at least 64 give every warp a tile.  The partial
-// results are bounded at 64 MB and 512 chunks, whatever the table's reach.
+// joins cost more); at least 64 give every warp a tile, and at least 128 where 64 would make more than a CTA an
+// SM, since a chunk's start, end and join take longer than its second 64 tokens (one sequence of 8191, 2 key heads:
+// 8.7 us, 10.1 with 64, 9.4 with 192; 4 of 8000: 9.8 and 14.9; one of 2000, 1 key head: 6.8 us with 64, 7.0 with 128).
+// The partial results are bounded at 64 MB and 512 chunks, whatever the table's reach.
 void plan_decode_attn(int64_t N, int64_t Hq, int64_t Hk, int64_t reach, int* chunk, int* splits) {
     const int64_t units = N * Hk * ((Hq / Hk + 15) / 16);
     reach += kTile;
     int64_t c = (units * reach + 148 * 8 - 1) / (148 * 8);
-    c = c < 64 ? 64 : (c > 512 ? 512 : c);
+    const int64_t least = units * reach <= 148 * 64 ? 64 : 128;
+    c = c < least ? least : (c > 512 ? 512 : c);
     int64_t most = (int64_t(1) << 24) / (N * Hq * 130);
     most = most < 1 ? 1 : (most > 512 ? 512 : most);
     if (c * most < reach) c = (reach + most - 1) / most;

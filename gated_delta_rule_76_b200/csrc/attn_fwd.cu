@@ -188,7 +188,6 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::kBar + 304);
     cx.abort_flag = reinterpret_cast<volatile int*>(sm + L::kBar + 308);
     cx.err = p.io.err;
-    cx.wait_ns = p.io.wait_ns ? p.io.wait_ns : kWaitNs;
     if (blockIdx.x == 0 && tid == 0) *cx.err = 0;  // every CTA is running, and none gives up a wait within microseconds
     if (sb & 1023u) {
         if (tid == 0) atomicOr(cx.err, 1);
@@ -248,8 +247,8 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
             if ((tid & 31) == 0 && *cx.abort_flag) {
                 // after an expired wait: the copies still on their way land before the memory is given up
-                if (owns) mbar_wait(cx.bars + B_Q, (owns - 1) & 1, cx.wait_ns);
-                for (int i = ri < NS ? 0 : ri - NS; i < ri; ++i) mbar_wait(cx.bars + B_R + i % NS, (i / NS) & 1, cx.wait_ns);
+                if (owns) mbar_wait(cx.bars + B_Q, (owns - 1) & 1, kWaitNs);
+                for (int i = ri < NS ? 0 : ri - NS; i < ri; ++i) mbar_wait(cx.bars + B_R + i % NS, (i / NS) & 1, kWaitNs);
             }
             __syncwarp();
         } else if (warp == kMmaWarp) {

@@ -22,7 +22,7 @@ namespace attn {
 
 using namespace gdn::tc;
 
-constexpr uint64_t kWaitNs = 4000000000ull;
+constexpr uint64_t kWaitNs = 4000000000ull;  // limit of one bounded wait
 constexpr int kRows = 128;
 constexpr int kNoWindow = 1 << 30;  // more than any sequence has; differences with it stay within 32 bits
 
@@ -148,7 +148,6 @@ struct Ctx {
     uint64_t* bars;
     volatile int* abort_flag;
     int* err;
-    uint64_t wait_ns;
 };
 
 // Bounded wait of one thread; on expiry the error word and the CTA's abort flag are set.  A try waits in
@@ -163,7 +162,7 @@ __device__ __forceinline__ bool wait_bar(const Ctx& cx, int bar, uint32_t parity
         if (*cx.abort_flag) return false;
         const uint64_t now = globaltimer_ns();
         if (!t0) t0 = now;
-        if (now - t0 > cx.wait_ns) {
+        if (now - t0 > kWaitNs) {
             *cx.abort_flag = 1;
             atomicOr(cx.err, 1);
             return false;
