@@ -97,6 +97,27 @@ def test_many_units_a_cta(lens, Hq, Hk, d, window):
         ref.within(g[name], x, b, name)
 
 
+@pytest.mark.parametrize("Hq,Hk,d,window", [(2, 1, 128, 0), (3, 3, 64, 700)])
+def test_a_long_sequence_in_a_padded_batch(Hq, Hk, d, window):
+    """Few units, cut into parts: what lies before and behind the sequence is neither read nor written."""
+    T, a, b = 2100, 50, 1900
+    q, k, v, do = (rnd(T, h, d, seed=s) for s, h in enumerate((Hq, Hk, Hk, Hq)))
+    want, bound, grads, bounds = ref.packed(*(t[a:b] for t in (q, k, v)), [0, b - a], d ** -0.5, window, do[a:b])
+    for t in (q, k, v, do):
+        t[:a] = t[b:] = float("nan")
+    cu = [a, b]
+    cache = cache_of(q, k, v, cu)
+    o = torch.full_like(q, float("nan"))
+    gdn.gdn_attn_fwd(q, k, v, cu, window=window, o=o, bwd_cache=cache)
+    held = [torch.full_like(t, 5.0) for t in (q, k, v)]
+    gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache, window=window, dq=held[0], dk=held[1], dv=held[2])
+    assert o[:a].isnan().all() and o[b:].isnan().all()
+    ref.within(o[a:b], want, bound, "o")
+    for t, x, y, name in zip(held, grads, bounds, ("dq", "dk", "dv")):
+        assert (t[:a] == 5.0).all() and (t[b:] == 5.0).all(), name
+        ref.within(t[a:b], x, y, name)
+
+
 def test_short_units_in_a_row_keep_the_copies_in_step():
     """Many units of one or two key tiles at heads of 64, whose ring of key tiles runs five pairs ahead: no wait may
     expire, and every run gives the same bits."""
@@ -313,3 +334,54 @@ def test_refusals_say_the_same_through_both(monkeypatch):
     got = [says(f) for f in bad]
     monkeypatch.setattr(gdn, "_native", None)
     assert got == [says(f) for f in bad]
+
+
+def test_offsets_past_32_bits_in_a_batch():
+    """2.4e9 elements of q: the last sequence's rows and gradients are those of a call over it alone."""
+    Hq, Hk, d, n, window = 64, 1, 128, 200, 64
+    T = 2 ** 31 // (Hq * d) + 30000
+    q, do = (torch.empty(T, Hq, d, dtype=BF, device="cuda").normal_() for _ in range(2))
+    k, v = (torch.empty(T, Hk, d, dtype=BF, device="cuda").normal_() for _ in range(2))
+    cu = [0, T - n, T]
+    cache = cache_of(q, k, v, cu)
+    o = gdn.gdn_attn_fwd(q, k, v, cu, window=window, bwd_cache=cache)
+    g = gdn.gdn_attn_bwd(q, k, v, cu, o, grad_o=do, fwd_cache=cache, window=window)
+    last = [t[T - n:].clone() for t in (q, k, v, do)]
+    c1 = cache_of(*last[:3], [0, n])
+    o1 = gdn.gdn_attn_fwd(*last[:3], [0, n], window=window, bwd_cache=c1)
+    assert torch.equal(o[T - n:], o1)
+    want, bound, grads, bounds = ref.packed(*last[:3], [0, n], d ** -0.5, window, last[3])
+    ref.within(o1, want, bound, "o")
+    for name, x, y in zip(("dq", "dk", "dv"), grads, bounds):
+        ref.within(g[name][T - n:], x, y, name)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    freq = torch.rand(32, device="cuda")
+    w = rnd(d)
+    y, _ = gdn.gdn_qk_norm_rope_fwd(q, None, pos, freq, q_norm_w=w)
+    y1, _ = gdn.gdn_qk_norm_rope_fwd(last[0], None, pos[T - n:].clone(), freq, q_norm_w=w)
+    assert torch.equal(y[T - n:], y1)
+    gx = gdn.gdn_qk_norm_rope_bwd(q, None, pos, freq, grad_q=do, q_norm_w=w)
+    g1 = gdn.gdn_qk_norm_rope_bwd(last[0], None, pos[T - n:].clone(), freq, grad_q=last[3], q_norm_w=w)
+    assert torch.equal(gx["dq"][T - n:], g1["dq"])
+
+
+def test_offsets_past_32_bits_in_a_cache():
+    """Pages behind the first 2^31 elements: appended, read back, attended."""
+    Hq, Hk, d, page = 4, 2, 128, 64
+    pages = 2 ** 31 // (page * Hk * d) + 8
+    kc, vc = (torch.empty(pages, page, Hk, d, dtype=BF, device="cuda") for _ in range(2))
+    ids = [pages - 1, 3, pages - 5, 0]
+    small = rnd(4, page, Hk, d, seed=1), rnd(4, page, Hk, d, seed=2)
+    for big, s in zip((kc, vc), small):
+        big[ids] = s
+    table = torch.tensor([[pages - 1, 3, pages - 5, 0]], dtype=torch.int32, device="cuda")
+    near = torch.tensor([[0, 1, 2, 3]], dtype=torch.int32, device="cuda")
+    ctx = torch.tensor([150], dtype=torch.int32, device="cuda")
+    q, k, v = (rnd(1, h, d, seed=s) for s, h in ((3, Hq), (4, Hk), (5, Hk)))
+    got, _ = gdn.gdn_kv_append(k, v, kc, vc, table, ctx, q=q)
+    want, _ = gdn.gdn_kv_append(k, v, *small, near, ctx, q=q)
+    assert torch.equal(got, want)
+    for big, s in zip((kc, vc), small):
+        assert torch.equal(big[ids], s)
+    ctx += 1
+    assert torch.equal(gdn.gdn_attn_decode(got, kc, vc, table, ctx), gdn.gdn_attn_decode(want, *small, near, ctx))
