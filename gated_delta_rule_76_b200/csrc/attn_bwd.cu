@@ -29,7 +29,7 @@
 // start as dkdv's end, and fill the SMs that have run out of key tiles.
 //
 // What bounds: dkdv's chain of P, dV, S (about 2980 cycles an item in a long call, of which the products take 2048) and
-// dq's element-wise work (2660 and 1536).  Forward and backward of 4 sequences of 2048, 16 heads of 128 on 4: 333 us, 723
+// dq's element-wise work (2660 and 1536).  Forward and backward of 4 sequences of 2048, 16 heads of 128 on 4: 338 us, 712
 // TFLOP/s of the formula's 7 products (the kernels compute 9), the tensor pipe active 51% of dkdv and 48% of dq.
 // Tried and slower: dkdv with S in halves, one of them ahead of dV (8%: the narrow products' time); 16 element-wise warps
 // (no difference).
