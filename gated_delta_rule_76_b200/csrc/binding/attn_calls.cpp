@@ -77,10 +77,10 @@ bool norm_of(PyObject* const* args, int64_t d, Inputs& in, gdn_qk_norm* n) {
     const Tensor *f = in.optional(args[0], at::kFloat, 1), *qw = in.optional(args[1], in.dtype, 1),
                  *kw = in.optional(args[2], in.dtype, 1);
     double eps, scale;
-    const int il = PyObject_IsTrue(args[4]);
-    if (!in.plain || !real(args[3], &eps) || !real(args[5], &scale) || il < 0) return false;
+    int64_t il;
+    if (!in.plain || !real(args[3], &eps) || !whole(args[4], &il) || !real(args[5], &scale)) return false;
     if ((qw && qw->size(0) != d) || (kw && kw->size(0) != d)) return false;
-    *n = gdn_qk_norm{at_of(qw), at_of(kw), static_cast<const float*>(at_of(f)), f ? 2 * f->size(0) : 0, il, (float)eps, (float)scale};
+    *n = gdn_qk_norm{at_of(qw), at_of(kw), static_cast<const float*>(at_of(f)), f ? 2 * f->size(0) : 0, (int32_t)il, (float)eps, (float)scale};
     return true;
 }
 

@@ -310,6 +310,7 @@ def test_refusals_say_the_same_through_both(monkeypatch):
         lambda: gdn.gdn_attn_fwd(q.float(), q.float(), q.float(), cu),          # bf16 only
         lambda: gdn.gdn_qk_norm_rope_fwd(q, k, None, torch.ones(8, device="cuda")),
         lambda: gdn.gdn_qk_norm_rope_fwd(q, k, norm_eps=-1.0),
+        lambda: gdn.gdn_qk_norm_rope_fwd(q, k, interleaved=2),
         lambda: gdn.gdn_qk_norm_rope_fwd(q, k, q_norm_w=rnd(32)),
         lambda: gdn.gdn_qk_norm_rope_fwd(rnd(8, 4, 32), None),
         lambda: gdn.gdn_kv_append(q, q, kc, kc, table, ctx),                    # 4 heads into a cache of 2
