@@ -8,8 +8,8 @@
 //     P = exp2(S c - m)    a thread a row: c = scale log2(e), running reference m and sum l
 //     O += P V             tcgen05, P as bf16 over S's columns (A in tensor memory), V as MN-major B
 // m is not moved for every new maximum: any reference within 2^8 of it serves as well (p stays below
-// 2^8, sums stay fp32, and bf16's relative rounding does not depend on it), so the O accumulator is
-// rescaled only when a row's maximum has outgrown m by more than 8.
+// 2^8, sums stay fp32, and bf16's relative rounding is no larger for it), so a row's part of the O accumulator is
+// rescaled only when its own maximum has outgrown m by more than 8.
 // P is rounded to bf16 because that is what the tensor cores multiply with bf16 V; l sums the unrounded p.
 //
 // One CTA an SM stays for the whole call and walks its units as one stream.  Warps 0-3 and 4-7 are the
@@ -324,9 +324,12 @@ attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
                     for (int e = 2; e < 32; e += 2) x[c] = max3(x[c], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
                 }
                 const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
-                if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                    const float mn = fmaxf(m, mx), f = m == -INFINITY ? 0.f : exp2_approx(m - mn);
-                    m = mn;
+                // Each row decides for itself; the vote only skips the work.  p's rounding goes by m, so that a row that moved
+                // with its warp's others would get other bits from padding, the next sequence's rows or later queries.
+                const bool move = mx > m + 8.f;
+                if (__any_sync(0xffffffffu, move)) {
+                    const float f = !move ? 1.f : m == -INFINITY ? 0.f : exp2_approx(m - mx);
+                    if (move) m = mx;
                     l *= f;
                     if (kt < hi) {
 #pragma unroll
