@@ -271,11 +271,13 @@ __global__ void __launch_bounds__(kThreads, Smem<D, ROWS16>::kCtas) decode_attn_
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
             x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2)) * scale_log2;
         }
-        if (__any_sync(0xffffffffu, x0 > m0 + 8.f || (ROWS16 && x1 > m1 + 8.f))) {
-            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-            const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0), f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-            m0 = n0;
-            m1 = n1;
+        // each row decides for itself, the vote only skips the work: a head's rounding of p, which goes by its reference,
+        // does not depend on the other heads of its group
+        const bool up0 = x0 > m0 + 8.f, up1 = ROWS16 && x1 > m1 + 8.f;
+        if (__any_sync(0xffffffffu, up0 || up1)) {
+            const float f0 = up0 ? ex2(m0 - x0) : 1.f, f1 = up1 ? ex2(m1 - x1) : 1.f;
+            if (up0) m0 = x0;
+            if (up1) m1 = x1;
             l0 *= f0;
             l1 *= f1;
 #pragma unroll

@@ -1,5 +1,5 @@
 """A row's result depends on its own query and the keys it sees alone, bit for bit: not on the rows that share its
-warp, whether they are padding, the next sequence's or later tokens of its own.
+warp, whether they are padding, the next sequence's, later tokens of its own or other heads of its group.
 
 The running reference of a row's softmax is what could carry such a dependence: p is rounded to bf16 against it.  The
 inputs below make the other rows' maximum jump in a key tile after their first, while the row's own does not."""
@@ -62,3 +62,19 @@ def test_forward_rows_do_not_see_later_queries(n, behind, Hq, Hk, d, window):
     b = gdn.gdn_attn_fwd(jump(q, k, slice(at, n), slice(None)), k, v, [0, n], window=window)
     assert torch.equal(a[:at], b[:at])
     assert not torch.equal(a[at:], b[at:])
+
+
+@pytest.mark.parametrize("Hq,Hk,d,page", [(4, 1, 64, 16), (8, 2, 128, 16), (16, 1, 128, 64), (4, 1, 128, 24)])
+def test_decode_heads_do_not_see_one_another(Hq, Hk, d, page):
+    """Eight sequences of 1500 tokens: chunks of 128, two tiles a warp."""
+    N, ctx, G = 8, 1500, Hq // Hk
+    pages = -(-ctx // page)
+    kc, vc = rnd(N * pages, page, Hk, d, seed=1), rnd(N * pages, page, Hk, d, seed=2)
+    table = torch.arange(N * pages, dtype=torch.int32, device="cuda").view(N, pages)
+    lens = torch.full((N,), ctx, dtype=torch.int32, device="cuda")
+    q = rnd(N, Hq, d, seed=3)
+    other = q.clone()
+    other.view(N, Hk, G, d)[:, :, 1:] *= 30
+    a, b = (gdn.gdn_attn_decode(x, kc, vc, table, lens).view(N, Hk, G, d) for x in (q, other))
+    assert torch.equal(a[:, :, 0], b[:, :, 0])
+    assert not torch.equal(a[:, :, 1:], b[:, :, 1:])
