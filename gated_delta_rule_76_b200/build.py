@@ -6,6 +6,7 @@ gated_delta_rule_76_b200/libgdn.so.  Usage: ``python -m gated_delta_rule_76_b200
 from __future__ import annotations
 
 import glob
+import importlib
 import os
 import shutil
 import subprocess
@@ -59,11 +60,20 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     _build_lib(SELFTEST_LIB, selftest_sources(), "selftest_", force, verbose, jobs)
     _build_lib(LIB, sources(), "", force, verbose, jobs)
     _build_binding(force, verbose)
+    _look_again()
     return LIB
 
 
+def _look_again():
+    """A binding that was looked for before it was built is looked for again at the next call."""
+    importlib.invalidate_caches()
+    gdn = sys.modules.get(f"{__package__}.gdn")
+    if gdn is not None and gdn.__dict__.get("_native", gdn) is None:
+        del gdn._native
+
+
 def _build_binding(force, verbose):
-    """The native marshalling of the attention layer's short calls, against torch's headers and libgdn.so."""
+    """The native marshalling of the attention layer's short calls, against torch's headers."""
     src = os.path.join(CSRC, "binding", "attn_calls.cpp")
     if not force and up_to_date(BINDING, [src]):
         return
@@ -74,8 +84,7 @@ def _build_binding(force, verbose):
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", tmp, "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
-           "-I", sysconfig.get_paths()["include"], "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
-           "-L", PKG, "-l:libgdn.so", "-Wl,-rpath,$ORIGIN"]
+           "-I", sysconfig.get_paths()["include"], "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

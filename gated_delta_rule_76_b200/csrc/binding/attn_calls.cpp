@@ -6,6 +6,8 @@
 //     None   where a tensor is anything else: gdn.py's general marshalling then takes the call, or says what is wrong,
 //     an int a gdn_status other than GDN_OK.
 // Sizes and values are checked where every caller's are, in the C calls.
+// The module is not linked to libgdn.so: gdn.py hands it the entry points of the copy that it has loaded (bind), so that
+// importing it maps no second one, and both ways call the same library whatever lies at its path by now.
 #include <Python.h>
 #include <ATen/ATen.h>
 #include <c10/cuda/CUDAFunctions.h>
@@ -20,6 +22,18 @@
 namespace {
 
 using at::Tensor;
+
+// libgdn's entry points that are called here, by name; NULL until bind.
+#define GDN_ENTRIES(X)                                                                                            \
+    X(gdn_qk_norm_rope_fwd) X(gdn_qk_norm_rope_bwd_workspace_size) X(gdn_qk_norm_rope_bwd)                        \
+    X(gdn_attn_fwd_workspace_size) X(gdn_attn_fwd) X(gdn_attn_bwd_workspace_size) X(gdn_attn_bwd)                 \
+    X(gdn_kv_append) X(gdn_attn_decode_workspace_size) X(gdn_attn_decode)
+struct Entries {
+#define X(f) decltype(&::f) f = nullptr;
+    GDN_ENTRIES(X)
+#undef X
+    bool bound = false;
+} lib;
 
 // The tensors of one call: all like the first in place, and each of its own type.
 struct Inputs {
@@ -138,7 +152,7 @@ bool qk_of(PyObject* const* args, Inputs& in, A* a, const Tensor** q, const Tens
 // (q, k or None, positions or None, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale) -> (q_out, k_out)
 PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 9) Py_RETURN_NONE;
+    if (n != 9 || !lib.bound) Py_RETURN_NONE;
     Inputs in;
     gdn_qk_fwd_args a{};
     const Tensor *q, *k;
@@ -147,7 +161,7 @@ PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     if (k) ko = at::empty(k->sizes(), k->options());
     a.q_out = qo.data_ptr();
     a.k_out = k ? ko.data_ptr() : nullptr;
-    const gdn_status s = unlocked([&] { return gdn_qk_norm_rope_fwd(&a, stream_of(in.device)); });
+    const gdn_status s = unlocked([&] { return lib.gdn_qk_norm_rope_fwd(&a, stream_of(in.device)); });
     if (s) return PyLong_FromLong(s);
     return tuple({&qo, k ? &ko : nullptr});
     END_HANDLE_TH_ERRORS
@@ -156,7 +170,7 @@ PyObject* qk_norm_rope_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // (the forward's nine, grad_q, grad_k or None) -> (dq, dk, dq_norm_w, dk_norm_w), None for those that do not apply
 PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 11) Py_RETURN_NONE;
+    if (n != 11 || !lib.bound) Py_RETURN_NONE;
     Inputs in;
     gdn_qk_bwd_args a{};
     const Tensor *q, *k;
@@ -174,7 +188,7 @@ PyObject* qk_norm_rope_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.grad_k = k ? dk.data_ptr() : nullptr;
     a.grad_q_norm_w = a.norm.q_norm_w ? dqw.data_ptr<float>() : nullptr;
     a.grad_k_norm_w = a.norm.k_norm_w ? dkw.data_ptr<float>() : nullptr;
-    const gdn_status s = run(gdn_qk_norm_rope_bwd, a, gdn_qk_norm_rope_bwd_workspace_size(&a), dq, in.device);
+    const gdn_status s = run(lib.gdn_qk_norm_rope_bwd, a, lib.gdn_qk_norm_rope_bwd_workspace_size(&a), dq, in.device);
     if (s) return PyLong_FromLong(s);
     return tuple({&dq, k ? &dk : nullptr, a.norm.q_norm_w ? &dqw : nullptr, a.norm.k_norm_w ? &dkw : nullptr});
     END_HANDLE_TH_ERRORS
@@ -207,7 +221,7 @@ bool attn_of(PyObject* qo, PyObject* ko, PyObject* vo, PyObject* cuo, PyObject* 
 // (q, k, v, cu_seqlens on the device, scale or None, window, bwd_cache or None) -> o
 PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 7) Py_RETURN_NONE;
+    if (n != 7 || !lib.bound) Py_RETURN_NONE;
     Inputs in;
     gdn_attn_fwd_args a{};
     const Tensor *q, *k;
@@ -218,7 +232,7 @@ PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.o = o.data_ptr();
     a.bwd_cache = cache ? cache->data_ptr() : nullptr;
     a.bwd_cache_bytes = cache ? (size_t)cache->size(0) : 0;
-    const gdn_status s = run(gdn_attn_fwd, a, gdn_attn_fwd_workspace_size(&a), o, in.device);
+    const gdn_status s = run(lib.gdn_attn_fwd, a, lib.gdn_attn_fwd_workspace_size(&a), o, in.device);
     return s ? PyLong_FromLong(s) : THPVariable_Wrap(o);
     END_HANDLE_TH_ERRORS
 }
@@ -226,7 +240,7 @@ PyObject* attn_fwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // (q, k, v, cu_seqlens on the device, scale or None, window, o, grad_o, fwd_cache) -> (dq, dk, dv)
 PyObject* attn_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 9) Py_RETURN_NONE;
+    if (n != 9 || !lib.bound) Py_RETURN_NONE;
     Inputs in;
     gdn_attn_bwd_args a{};
     const Tensor *q, *k;
@@ -241,7 +255,7 @@ PyObject* attn_bwd(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.grad_v = dv.data_ptr();
     a.fwd_cache = cache->data_ptr();
     a.fwd_cache_bytes = (size_t)cache->size(0);
-    const gdn_status s = run(gdn_attn_bwd, a, gdn_attn_bwd_workspace_size(&a), dq, in.device);
+    const gdn_status s = run(lib.gdn_attn_bwd, a, lib.gdn_attn_bwd_workspace_size(&a), dq, in.device);
     if (s) return PyLong_FromLong(s);
     return tuple({&dq, &dk, &dv});
     END_HANDLE_TH_ERRORS
@@ -268,7 +282,7 @@ bool cache_of(PyObject* const* args, Inputs& in, int64_t nseq, int64_t Hk, int64
 // k_norm_w, norm_eps, interleaved, rot_scale, want_k) -> (q_out, k_out)
 PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 15) Py_RETURN_NONE;
+    if (n != 15 || !lib.bound) Py_RETURN_NONE;
     Inputs in;
     const Tensor* k = in.first(args[0], 3);
     if (!k) Py_RETURN_NONE;
@@ -293,7 +307,7 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.k_out = want_k ? ko.data_ptr() : nullptr;
     a.Hq = q ? q->size(1) : 0;
     a.dtype = dtype_of(in.dtype);
-    const gdn_status s = unlocked([&] { return gdn_kv_append(&a, stream_of(in.device)); });
+    const gdn_status s = unlocked([&] { return lib.gdn_kv_append(&a, stream_of(in.device)); });
     if (s) return PyLong_FromLong(s);
     return tuple({q ? &qo : nullptr, want_k ? &ko : nullptr});
     END_HANDLE_TH_ERRORS
@@ -302,7 +316,7 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
 // (q, k_cache, v_cache, block_table, context_lens, scale or None, window, max_context) -> o
 PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
     HANDLE_TH_ERRORS
-    if (n != 8) Py_RETURN_NONE;
+    if (n != 8 || !lib.bound) Py_RETURN_NONE;
     Inputs in;
     const Tensor* q = in.first(args[0], 3);
     if (!q || !THPVariable_Check(args[1]) || THPVariable_Unpack(args[1]).dim() != 4) Py_RETURN_NONE;
@@ -320,9 +334,50 @@ PyObject* attn_decode(PyObject*, PyObject* const* args, Py_ssize_t n) {
     a.o = o.data_ptr();
     a.scale = (float)scale;
     a.dtype = dtype_of(in.dtype);
-    const gdn_status s = run(gdn_attn_decode, a, gdn_attn_decode_workspace_size(&a), o, in.device);
+    const gdn_status s = run(lib.gdn_attn_decode, a, lib.gdn_attn_decode_workspace_size(&a), o, in.device);
     return s ? PyLong_FromLong(s) : THPVariable_Wrap(o);
     END_HANDLE_TH_ERRORS
+}
+
+// ({name: address} of every entry point) -> None
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+    if (n != 1 || !PyDict_Check(args[0])) {
+        PyErr_SetString(PyExc_TypeError, "bind takes the entry points' addresses by name");
+        return nullptr;
+    }
+    Entries e;
+#define X(f)                                                                        \
+    {                                                                               \
+        PyObject* o = PyDict_GetItemString(args[0], #f); /* borrowed */             \
+        void* p = o && PyLong_Check(o) ? PyLong_AsVoidPtr(o) : nullptr;             \
+        if (!p) {                                                                   \
+            if (!PyErr_Occurred()) PyErr_SetString(PyExc_KeyError, #f);             \
+            return nullptr;                                                         \
+        }                                                                           \
+        e.f = reinterpret_cast<decltype(e.f)>(p);                                   \
+    }
+    GDN_ENTRIES(X)
+#undef X
+    e.bound = true;
+    lib = e;
+    Py_RETURN_NONE;
+}
+
+// The names that bind takes.
+PyObject* entries(PyObject*, PyObject* const*, Py_ssize_t) {
+    const char* names[] = {
+#define X(f) #f,
+        GDN_ENTRIES(X)
+#undef X
+    };
+    constexpr Py_ssize_t count = sizeof(names) / sizeof(names[0]);
+    PyObject* t = PyTuple_New(count);
+    for (Py_ssize_t i = 0; t && i < count; ++i) {
+        PyObject* o = PyUnicode_FromString(names[i]);
+        if (!o) Py_CLEAR(t);
+        else PyTuple_SET_ITEM(t, i, o);
+    }
+    return t;
 }
 
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
@@ -331,7 +386,7 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef methods[] = {method<qk_norm_rope_fwd>("qk_norm_rope_fwd"), method<qk_norm_rope_bwd>("qk_norm_rope_bwd"),
                          method<attn_fwd>("attn_fwd"), method<attn_bwd>("attn_bwd"), method<kv_append>("kv_append"),
-                         method<attn_decode>("attn_decode"), {nullptr, nullptr, 0, nullptr}};
+                         method<attn_decode>("attn_decode"), method<bind>("bind"), method<entries>("entries"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_attn_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -627,10 +627,34 @@ def gdn_layer_core_bwd(xq, xk, xv, conv_w, alpha, z, grad_y, b=None, w=None, bet
 # their arguments are plain (csrc/binding/attn_calls.cpp: 5 to 8 us a call instead of 13 to 17); the marshalling below
 # takes every other case.
 # ---------------------------------------------------------------------------------------------
-try:
-    from . import _attn_calls as _native
-except ImportError:  # not built: everything goes the general way
-    _native = None
+def _find_native():
+    """The native module, calling the library that load() has opened; None where it is not built: every call then goes the
+    general way.  Not looked for on import: a program that reads the package's inputs, or builds the library, maps none of it."""
+    global _native
+    lib = load()
+    try:
+        from . import _attn_calls as native
+    except ImportError:
+        native = None
+    if native is not None:
+        native.bind({name: ctypes.cast(getattr(lib, name), P).value for name in native.entries()})
+    _native = native
+    return native
+
+
+def __getattr__(name):  # _native before the first call
+    if name == "_native":
+        return _find_native()
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+
+
+def _native_calls():
+    try:
+        return _native
+    except NameError:
+        return _find_native()
+
+
 _AS_IS = contextlib.nullcontext()
 # what torch.cuda.current_device and current_stream come down to once CUDA is up, as it is where a CUDA tensor exists
 _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
@@ -743,8 +767,8 @@ def gdn_qk_norm_rope_fwd(q, k, positions=None, inv_freq=None, *, q_norm_w=None, 
                          q_out=None, k_out=None, stream=None):
     """Per-head RMS norm of q [T,Hq,d] and k [T,Hk,d] (or None) and the rotation of their first
     ``2 * len(inv_freq)`` channels by ``positions`` [T] int32.  Returns (q_out, k_out)."""
-    if stream is None and q_out is None and k_out is None and _native is not None:
-        r = _native.qk_norm_rope_fwd(q, k, positions, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
+    if stream is None and q_out is None and k_out is None and (native := _native_calls()) is not None:
+        r = native.qk_norm_rope_fwd(q, k, positions, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale)
         if r is not None:
             return r if type(r) is tuple else check(r, "gdn_qk_norm_rope_fwd")
     with _on(q, stream):
@@ -766,8 +790,8 @@ def gdn_qk_norm_rope_bwd(q, k, positions=None, inv_freq=None, *, grad_q, grad_k=
                          workspace: Optional[torch.Tensor] = None, stream=None) -> Dict[str, torch.Tensor]:
     """Reverse mode of gdn_qk_norm_rope_fwd for the gradients ``grad_q``, ``grad_k`` of its results.
     Returns dq, dk in the inputs' dtype and dq_norm_w, dk_norm_w [d] fp32 (those that apply)."""
-    if stream is None and workspace is None and _native is not None:
-        r = _native.qk_norm_rope_bwd(q, k, positions, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale, grad_q, grad_k)
+    if stream is None and workspace is None and (native := _native_calls()) is not None:
+        r = native.qk_norm_rope_bwd(q, k, positions, inv_freq, q_norm_w, k_norm_w, norm_eps, interleaved, rot_scale, grad_q, grad_k)
         if r is not None:
             names = ("dq", "dk", "dq_norm_w", "dk_norm_w")
             return {n: t for n, t in zip(names, r) if t is not None} if type(r) is tuple else check(r, "gdn_qk_norm_rope_bwd")
@@ -816,8 +840,8 @@ def gdn_attn_fwd(q, k, v, cu_seqlens, *, scale: Optional[float] = None, window: 
     [nseq + 1] (int32 on the device, or a list or CPU tensor, which is checked).  ``scale``: d ** -0.5
     unless given; ``window``: 0, or how many tokens, itself included, a token sees.  Returns o; rows
     outside every sequence stay as they were (unset in an ``o`` made here)."""
-    if stream is None and o is None and workspace is None and _native is not None:
-        r = _native.attn_fwd(q, k, v, cu_seqlens, scale, window, bwd_cache)
+    if stream is None and o is None and workspace is None and (native := _native_calls()) is not None:
+        r = native.attn_fwd(q, k, v, cu_seqlens, scale, window, bwd_cache)
         if r is not None:
             return r if type(r) is not int else check(r, "gdn_attn_fwd")
     with _on(q, stream):
@@ -840,8 +864,8 @@ def gdn_attn_bwd(q, k, v, cu_seqlens, o, *, grad_o, fwd_cache: torch.Tensor, sca
                  stream=None) -> Dict[str, torch.Tensor]:
     """Reverse mode of gdn_attn_fwd from its output ``o`` and the cache it filled.  Returns dq, dk, dv
     in bf16 (``dq``, ``dk``, ``dv``: buffers to fill; rows outside every sequence stay as they were)."""
-    if stream is None and dq is None and dk is None and dv is None and workspace is None and _native is not None:
-        r = _native.attn_bwd(q, k, v, cu_seqlens, scale, window, o, grad_o, fwd_cache)
+    if stream is None and dq is None and dk is None and dv is None and workspace is None and (native := _native_calls()) is not None:
+        r = native.attn_bwd(q, k, v, cu_seqlens, scale, window, o, grad_o, fwd_cache)
         if r is not None:
             return dict(zip(("dq", "dk", "dv"), r)) if type(r) is tuple else check(r, "gdn_attn_bwd")
     with _on(q, stream):
@@ -882,8 +906,8 @@ def gdn_kv_append(k, v, k_cache, v_cache, block_table, context_lens, *, cu_seqle
     before (unchanged); ``cu_seqlens``: the sequences' new tokens, None for one each.  With ``q``
     [T,Hq,d], the same norm and rotation of q.  Returns (q_out or None, k_out or None: the keys as
     cached, with ``want_k``)."""
-    if stream is None and q_out is None and k_out is None and _native is not None:
-        r = _native.kv_append(k, v, k_cache, v_cache, block_table, context_lens, cu_seqlens, q, inv_freq, q_norm_w, k_norm_w,
+    if stream is None and q_out is None and k_out is None and (native := _native_calls()) is not None:
+        r = native.kv_append(k, v, k_cache, v_cache, block_table, context_lens, cu_seqlens, q, inv_freq, q_norm_w, k_norm_w,
                               norm_eps, interleaved, rot_scale, want_k)
         if r is not None:
             return r if type(r) is tuple else check(r, "gdn_kv_append")
@@ -915,8 +939,8 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, context_lens, *, scale: Op
     """One query token for N sequences, q [N,Hq,d], over the paged caches: ``context_lens`` [N] int32
     tokens each, this one's included.  ``max_context``: a bound on the lengths that the caller knows
     (0: the block table's reach).  Returns o [N,Hq,d]."""
-    if stream is None and o is None and workspace is None and _native is not None:
-        r = _native.attn_decode(q, k_cache, v_cache, block_table, context_lens, scale, window, max_context)
+    if stream is None and o is None and workspace is None and (native := _native_calls()) is not None:
+        r = native.attn_decode(q, k_cache, v_cache, block_table, context_lens, scale, window, max_context)
         if r is not None:
             return r if type(r) is not int else check(r, "gdn_attn_decode")
     with _on(q, stream):
