@@ -6,7 +6,6 @@ gated_delta_rule_76_b200/libgdn.so.  Usage: ``python -m gated_delta_rule_76_b200
 from __future__ import annotations
 
 import glob
-import importlib
 import os
 import shutil
 import subprocess
@@ -21,7 +20,6 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
 SELFTEST_LIB = os.path.join(PKG, "libgdn_selftest.so")
-BINDING = os.path.join(PKG, "_attn_calls.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -55,6 +53,12 @@ def up_to_date(lib, srcs) -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps(srcs))
 
 
+def binding() -> str:
+    """Path of the binding's native module for this torch and this Python, whose ABI it takes."""
+    import torch
+    return os.path.join(PKG, f"_attn_calls-torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
     """Build libgdn.so, the binding's native module and the test-only libgdn_selftest.so; returns the libgdn.so path."""
     _build_lib(SELFTEST_LIB, selftest_sources(), "selftest_", force, verbose, jobs)
@@ -66,7 +70,6 @@ def build(force: bool = False, verbose: bool = False, jobs: int = 0) -> str:
 
 def _look_again():
     """A binding that was looked for before it was built is looked for again at the next call."""
-    importlib.invalidate_caches()
     gdn = sys.modules.get(f"{__package__}.gdn")
     if gdn is not None and gdn.__dict__.get("_native", gdn) is None:
         del gdn._native
@@ -75,13 +78,14 @@ def _look_again():
 def _build_binding(force, verbose):
     """The native marshalling of the attention layer's short calls, against torch's headers."""
     src = os.path.join(CSRC, "binding", "attn_calls.cpp")
-    if not force and up_to_date(BINDING, [src]):
+    path = binding()
+    if not force and up_to_date(path, [src]):
         return
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
-    tmp = BINDING + ".tmp"
+    tmp = path + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", src, "-o", tmp, "-I", INCLUDE, "-isystem", inc,
            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
            "-I", sysconfig.get_paths()["include"], "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
@@ -90,7 +94,7 @@ def _build_binding(force, verbose):
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, path)
 
 
 def _build_lib(lib, srcs, prefix, force, verbose, jobs):

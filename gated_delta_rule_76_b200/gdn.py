@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
 from typing import Dict, Optional, Tuple
 
@@ -631,13 +632,17 @@ def _find_native():
     """The native module, calling the library that load() has opened; None where it is not built: every call then goes the
     general way.  Not looked for on import: a program that reads the package's inputs, or builds the library, maps none of it."""
     global _native
-    lib = load()
-    try:
-        from . import _attn_calls as native
-    except ImportError:
-        native = None
-    if native is not None:
-        native.bind({name: ctypes.cast(getattr(lib, name), P).value for name in native.entries()})
+    from .build import binding
+    lib, native, path = load(), None, binding()
+    if os.path.exists(path):
+        spec = importlib.util.spec_from_file_location(f"{__package__}._attn_calls", path)
+        try:
+            native = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(native)
+        except ImportError:  # against other libraries than this host's
+            native = None
+        else:
+            native.bind({name: ctypes.cast(getattr(lib, name), P).value for name in native.entries()})
     _native = native
     return native
 

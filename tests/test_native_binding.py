@@ -45,8 +45,9 @@ def package(built, tmp_path):
     to = tmp_path / "gated_delta_rule_76_b200"
     os.mkdir(to)
     for name in os.listdir(gbuild.PKG):
-        if name.endswith(".py") or (name.startswith("_attn_calls") and name.endswith(".so")):
+        if name.endswith(".py"):
             shutil.copy2(os.path.join(gbuild.PKG, name), to)
+    shutil.copy2(gbuild.binding(), to)
     stand_in(str(to / "libgdn.so"), 1)
     stand_in(str(tmp_path / "new.so"), 2)
     return tmp_path
@@ -82,9 +83,8 @@ assert len([m for m in mapped() if m[0].startswith("libgdn.so")]) == 1, mapped()
 
 def test_a_module_built_after_the_first_call_is_found(package):
     run("""
-import glob
 from gated_delta_rule_76_b200 import build, gdn
-module, = glob.glob("gated_delta_rule_76_b200/_attn_calls*.so")
+module = build.binding()
 os.rename(module, "kept.so")
 assert gdn._native is None and gdn._native_calls() is None
 os.rename("kept.so", module)
@@ -116,3 +116,30 @@ except TypeError:
 else:
     assert False
 """, ROOT)
+
+
+def test_a_module_of_another_torch_is_left_alone(package):
+    run("""
+import torch
+torch.__version__ = "1.0"
+from gated_delta_rule_76_b200 import gdn
+assert gdn.load().gdn_version() == 1 and gdn._native is None
+""", package)
+
+
+def test_a_file_that_is_no_module_is_left_alone(package):
+    run("""
+from gated_delta_rule_76_b200 import build, gdn
+open(build.binding(), "w").write("no library")
+assert gdn.load().gdn_version() == 1 and gdn._native is None
+""", package)
+
+
+def test_the_module_belongs_to_one_torch_and_one_python(monkeypatch):
+    import torch
+    here = gbuild.binding()
+    monkeypatch.setattr(torch, "__version__", "1.0")
+    assert gbuild.binding() != here
+    monkeypatch.undo()
+    monkeypatch.setattr(gbuild.sysconfig, "get_config_var", lambda name: ".cpython-311.so")
+    assert gbuild.binding() != here
