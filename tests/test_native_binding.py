@@ -135,6 +135,25 @@ assert gdn.load().gdn_version() == 1 and gdn._native is None
 """, package)
 
 
+@pytest.mark.parametrize("compiler", ["fails", "is missing"])
+def test_a_host_without_the_headers_keeps_the_library(compiler, monkeypatch, tmp_path):
+    """The module is optional, also when it is built; what an older source left is taken away."""
+    path = str(tmp_path / "module.so")
+    open(path, "w").close()
+
+    def run(cmd, **kw):
+        assert cmd[0] == "g++"
+        if compiler == "is missing":
+            raise FileNotFoundError("no g++")
+        return subprocess.CompletedProcess(cmd, 1, "", "no torch/csrc/Exceptions.h")
+
+    monkeypatch.setattr(gbuild, "binding", lambda: path)
+    monkeypatch.setattr(gbuild.subprocess, "run", run)
+    with pytest.warns(UserWarning, match="native module is not built"):
+        gbuild._build_binding(True, False)
+    assert not os.path.exists(path)
+
+
 def test_the_module_belongs_to_one_torch_and_one_python(monkeypatch):
     import torch
     here = gbuild.binding()
