@@ -295,7 +295,8 @@ PyObject* kv_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
         Py_RETURN_NONE;
     a.nseq = cu ? cu->size(0) - 1 : a.T;
     const int want_k = PyObject_IsTrue(args[14]);
-    if (!cache_of(args + 2, in, a.nseq, a.Hk, a.d, &a) || !norm_of(args + 8, a.d, in, &a.norm) || want_k < 0) Py_RETURN_NONE;
+    if (want_k < 0) return nullptr;
+    if (!cache_of(args + 2, in, a.nseq, a.Hk, a.d, &a) || !norm_of(args + 8, a.d, in, &a.norm)) Py_RETURN_NONE;
     Tensor qo, ko;
     if (q) qo = at::empty(q->sizes(), q->options());
     if (want_k) ko = at::empty(k->sizes(), k->options());
