@@ -676,9 +676,9 @@ def _on(t: torch.Tensor, stream):
         return _AS_IS if t.get_device() == _current_device() else torch.cuda.device(t.device)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=t.device)
+    if stream.device != t.device:
+        raise GdnError(f"a stream of {stream.device} for tensors on {t.device}")
     return torch.cuda.stream(stream)
-
-
 
 
 def _unexpected(name, t, shape, dtype, device):

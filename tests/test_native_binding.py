@@ -162,3 +162,14 @@ def test_the_module_belongs_to_one_torch_and_one_python(monkeypatch):
     monkeypatch.undo()
     monkeypatch.setattr(gbuild.sysconfig, "get_config_var", lambda name: ".cpython-311.so")
     assert gbuild.binding() != here
+
+
+def test_a_stream_of_another_device_is_refused():
+    """The tensors' device decides where a call runs: a stream of another one would be passed over in silence."""
+    import types
+
+    import torch
+    t = types.SimpleNamespace(is_cuda=True, device=torch.device("cuda", 0), get_device=lambda: 0)
+    other = types.SimpleNamespace(cuda_stream=77, device=torch.device("cuda", 1))
+    with pytest.raises(gdn.GdnError, match="stream of cuda:1 .* cuda:0"):
+        gdn._on(t, other)
