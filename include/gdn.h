@@ -565,8 +565,9 @@ GDN_API gdn_status gdn_attn_bwd(const gdn_attn_bwd_args* args, void* workspace, 
  * gdn_kv_append: the new tokens' k, normalised and rotated at their cache position, and v into the cache;
  * with q, the same tokens' q, normalised and rotated, into q_out.  Token i of sequence s takes position
  * context_lens[s] + i, context_lens being the tokens cached before (the call does not change it).
- * cu_seqlens NULL: one new token a sequence (T = nseq).  Two tokens sent to one slot leave either there.
- * Tokens outside every sequence are left out. */
+ * cu_seqlens NULL: one new token a sequence (T = nseq).  Tokens outside every sequence are left out.  Two tokens sent to
+ * one slot (of sequences that share a page) leave a mixture there: each value is one of the two's, and k and v need not
+ * agree on which; no order among tokens is kept. */
 typedef struct gdn_kv_append_args {
     const void* q;              /* [T,Hq,d] dtype, or NULL (then Hq = 0) */
     const void* k;              /* [T,Hk,d] dtype */

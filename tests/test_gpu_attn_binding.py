@@ -1,5 +1,5 @@
 """Arguments of the attention layer's calls that Python itself has to judge say the same through the native marshalling
-and the general one."""
+and the general one; and tokens that share a slot of the cache."""
 import pytest
 import torch
 
@@ -47,3 +47,18 @@ def test_errors_of_an_argument_reach_the_caller(native, monkeypatch):
     with pytest.raises(TypeError):
         gdn.gdn_attn_decode(k, kc, vc, table, ctx, max_context=1.5)
     assert gdn.kernel_launches() == before
+
+
+def test_tokens_in_one_slot_leave_values_of_either():
+    """Two sequences whose tables name the same page: every value there is one of the two tokens', nothing else changes."""
+    N, Hk, d, page = 64, 2, 128, 16
+    kc, vc = rnd(4, page, Hk, d, seed=1), rnd(4, page, Hk, d, seed=2)
+    kc0, vc0 = kc.clone(), vc.clone()
+    k, v = rnd(N, Hk, d, seed=3), rnd(N, Hk, d, seed=4)
+    table = torch.full((N, 1), 2, dtype=torch.int32, device="cuda")
+    ctx = torch.full((N,), 5, dtype=torch.int32, device="cuda")
+    gdn.gdn_kv_append(k, v, kc, vc, table, ctx)
+    for cache, held, new in ((kc, kc0, k), (vc, vc0, v)):
+        assert (cache[2, 5] == new).any(0).all()
+        held[2, 5] = cache[2, 5]
+        assert torch.equal(cache, held)
