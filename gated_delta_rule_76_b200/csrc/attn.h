@@ -95,10 +95,14 @@ struct AttnIO {
 inline int64_t attn_tiles(int64_t T, int64_t nseq) { return T / 128 + (nseq < T ? nseq : T); }
 // Parts that dkdv cuts a key tile's unit into.  The heaviest unit, the first key tile of a sequence with all the
 // group's queries, takes as long as the SMs' average of dkdv's and dq's work together at 160 units (one sequence or
-// several equal ones), or at 80 where a window makes the units alike; with fewer it would be what the call waits for
+// several equal ones), or at 80 where a window makes the units alike (one shorter than half of the call's tokens is taken
+// to: the sequences' lengths are not known here); with fewer it would be what the call waits for
 // (backward of 4096 tokens, 16 heads on 2: 515 us whole, 247 us in 3 parts; one sequence of 2600, 8 heads on 1: 344 and
 // 86 us).  A part costs its sums' way through memory (4 x 2048 tokens, 16 heads on 4, 272 units: 266 us whole, 314 us in 2
-// parts), and is worth it from two items on.
+// parts), and is worth it from two items on.  Where the two meet depends on the group: long sequences of 4 and more heads
+// on one gain up to the 192 units of the limit, small groups lose from 130 on.  Two parts and whole, us: 161 units of 20480
+// tokens, 8 heads on 1 2724 and 3021, 1 on 1 470 and 345; 168 units of 2600 tokens, 32 heads on 8 248 and 244, 8 on 8 104
+// and 68.  The limit takes the long calls' side.
 inline int attn_bwd_parts(int64_t T, int64_t nseq, int64_t Hq, int64_t Hk, int64_t window) {
     const int64_t units = attn_tiles(T, nseq) * Hk, items = Hq / Hk * ((T + 127) / 128);
     const int64_t want = window > 0 && window < T / 2 ? 80 : 192;
@@ -111,7 +115,8 @@ inline int attn_bwd_parts(int64_t T, int64_t nseq, int64_t Hq, int64_t Hk, int64
 // row's key tiles, one after the other, are what the call waits for: 2 us a tile, 1.6 with heads of 64.  A part has its own
 // start and end, 5 us, and its sums' way through memory and the joining kernel.  The sequences' lengths are not known
 // here: the longest is taken as twice what is left for one more (8192 tokens, 4 heads on 1: 124 us whole, 84 us in 2 parts;
-// 1783 and 7 tokens, 3 heads: 32 and 25 us; 1777, 16 heads, left whole: 33 us, 47 in 3 parts).
+// 1783 and 7 tokens, 3 heads: 32 and 25 us; 1777, 16 heads, left whole: 33 us, 47 in 3 parts).  Many short sequences beside
+// a long one make it look shorter than it is: the 8192 tokens with 15 sequences of one token are left whole (127 us).
 inline int attn_fwd_parts(int64_t T, int64_t nseq, int64_t Hq, int64_t d, int64_t window) {
     if (T < 1 || nseq < 1) return 1;
     const double units = (double)((attn_tiles(T, nseq) * Hq + 1) / 2), sums = (double)(T * Hq * d) * 4.0;

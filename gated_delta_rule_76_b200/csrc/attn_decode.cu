@@ -17,6 +17,9 @@
 // (plan_decode_attn); the warps of a CTA are joined in shared memory and the chunks of a sequence by
 // combine_kernel, both in index order, so results do not depend on timing.
 //
+// The compiler reports spills of 8 (pages of 16s) and 36 bytes at d = 128 with up to 8 heads a group, whose 168 registers
+// are what three CTAs an SM leave.
+//
 // Measured, d = 128: 256 sequences of 64 to 4500 tokens, 16 heads on 2: 58.6 us, 4.7 TB/s (a copy: 6.5); one sequence of 8191
 // tokens: 8.7 us, two kernels' latency (8.4 MB would take 1.3).
 #include <cuda_bf16.h>
@@ -462,7 +465,11 @@ cudaError_t launch_d(DecodeAttnParams p, cudaStream_t st) {
 // joins cost more); at least 64 give every warp a tile, and at least 128 where 64 would make more than a CTA an
 // SM, since a chunk's start, end and join take longer than its second 64 tokens (one sequence of 8191, 2 key heads:
 // 8.7 us, 10.1 with 64, 9.4 with 192; 4 of 8000: 9.8 and 14.9; one of 2000, 1 key head: 6.8 us with 64, 7.0 with 128).
-// The partial results are bounded at 64 MB and 512 chunks, whatever the table's reach.
+// The partial results are bounded at 64 MB and 512 chunks, whatever the table's reach: beyond them, chunks grow.
+// The contexts are not known here, so that a reach far above them costs chunks that are too long and CTAs that find
+// nothing to do, which max_context avoids.  Tables for 4500, 32768 and 131072 tokens under the 256 sequences of up to
+// 4500: 58.4, 70.6 and 101.7 us, with max_context 58 us each; one sequence of 8191 under 8192, 131072 and 2^20: 8.6, 10.4
+// and 28.7 us, with it 8.6 us each.
 void plan_decode_attn(int64_t N, int64_t Hq, int64_t Hk, int64_t reach, int* chunk, int* splits) {
     const int64_t units = N * Hk * ((Hq / Hk + 15) / 16);
     reach += kTile;

@@ -25,6 +25,7 @@
 // the two tiles share each copy of K and V), the exponentials as long (16 a cycle and SM).  A prompt of 16384
 // tokens, 8 heads of 128 on one: 440 us, 1250 TFLOP/s, the tensor pipe active 57% of the time.  At a unit's end the CTA
 // waits about 3500 cycles more for the last P V, the rows on their way out and the first masked tile.
+// Of the kernels only those of heads of 128 that keep the cache, whole, spill: 4 bytes (pairs of heads) and 40.
 // Where units are few, each is cut into parts of its key tiles (attn.h), whose sums against their own references go through
 // the workspace in fp32 and are joined by a second kernel.
 // Tried and slower: 3 of 8 exponentials by a polynomial on the FMA pipe (514 us instead of 447: the softmax's

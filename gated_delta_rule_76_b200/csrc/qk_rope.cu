@@ -19,7 +19,8 @@
 // takes is enough loads in flight (the rows of a batch are all loaded before the first is used) and few
 // instructions a channel (no exchange between lanes but the row's sum; packed fp32 pairs).
 // Measured, d = 128 in bf16: 32768 tokens of 16 + 4 heads forward and backward 177 us, 4.7 TB/s (a copy: 6.5);
-// 4099 tokens of 128 + 16 heads forward 57 us, 5.2 TB/s; two tokens 3.2 us.  Tried and slower: five CTAs an SM (262 us:
+// 4099 tokens of 128 + 16 heads forward 57 us, 5.2 TB/s; two tokens 3.2 us.  In fp32, the 32768 tokens: forward 122 us, 5.5
+// TB/s, backward 214 us, 4.7 TB/s, the latter with 48 to 52 bytes of spills at its 128 registers.  Tried and slower: five CTAs an SM (262 us:
 // spills), batches of 2 rows (186 us), the backward's rows through a private ring in shared memory (189 us).
 #include <cuda_bf16.h>
 
@@ -375,7 +376,10 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const QkParams p, in
 //     dw = sum over rows of gn x r,     dx = r (gn w - x r^2 mean(gn w x)).
 // The first `ctas_q` CTAs take q's rows, the others k's, each walking the tokens in a fixed stride; dw stays in
 // registers, 16 channels a lane, until a CTA adds its warps' in shared memory and stores one
-// partial; rope_dw_kernel adds the CTAs'.  Every order is fixed by the sizes.
+// partial; rope_dw_kernel adds the CTAs'.  Every order is fixed by the sizes.  All in fp32: a lane's own sum runs over its
+// rows of the tokens its warp takes (32768 tokens of 16 + 4 heads: 84 rows of q), and the chains behind it over 16 rows,
+// 13 partials and 32 slices, so that no term takes part in more than about 150 roundings.
+// A token's heads are one warp's: 64 tokens of 64 + 8 heads take 12.5 us (fp32: 17.8), the forward, which shares them, 3.7.
 template <class T, int D, bool IL>
 __global__ void __launch_bounds__(kThreads, 4) rope_bwd_kernel(const QkParams p, T* __restrict__ dq, T* __restrict__ dk,
                                                                int ctas_q) {

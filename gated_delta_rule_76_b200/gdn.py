@@ -943,7 +943,7 @@ def gdn_attn_decode(q, k_cache, v_cache, block_table, context_lens, *, scale: Op
                     max_context: int = 0, o=None, workspace: Optional[torch.Tensor] = None, stream=None):
     """One query token for N sequences, q [N,Hq,d], over the paged caches: ``context_lens`` [N] int32
     tokens each, this one's included.  ``max_context``: a bound on the lengths that the caller knows
-    (0: the block table's reach).  Returns o [N,Hq,d]."""
+    (0: the block table's reach, by which the work is then split: give it where the table is much wider).  Returns o [N,Hq,d]."""
     if stream is None and o is None and workspace is None and (native := _native_calls()) is not None:
         r = native.attn_decode(q, k_cache, v_cache, block_table, context_lens, scale, window, max_context)
         if r is not None:

@@ -509,7 +509,8 @@ GDN_API gdn_status gdn_qk_norm_rope_bwd(const gdn_qk_bwd_args* args, void* works
  *     s_ij = scale q_i . k_j  for j <= i (and j > i - window),   o_i = sum_j softmax_j(s_ij) v_j
  * with i, j the tokens of one sequence.  bf16 only (GDN_ERR_UNSUPPORTED otherwise).  Within a
  * sequence the values must be finite: a NaN or infinity in one token's k or v can reach any
- * output of its sequence, but none of another one.  The workspace starts with the status word that
+ * output of its sequence, but none of another one.  With the same sizes a token's output has the
+ * same bits whatever the tokens hold that it does not see.  The workspace starts with the status word that
  * gdn_workspace_status reads.  A strided q, k or v whose address and stride are multiples of 16
  * bytes is read in place, any other strided one from a dense copy in the workspace. */
 typedef struct gdn_attn_fwd_args {
@@ -590,8 +591,9 @@ GDN_API gdn_status gdn_kv_append(const gdn_kv_append_args* args, gdn_stream stre
 /* One query token a sequence over the paged cache: o_n = sum_j softmax_j(scale q_n . k_j) v_j over the
  * context_lens[n] cached tokens (with a window, the last `window` of them).  A sequence whose length is 0,
  * or whose every page is out of range, gets o = 0.  max_context bounds the lengths (longer ones are read as
- * max_context) and sets how the work is split; 0: max_pages * page_size.  The partial results of a split
- * context are joined in a fixed order. */
+ * max_context) and sets how the work is split; 0: max_pages * page_size.  The lengths themselves lie on the device, so
+ * that a block table much wider than they are makes a slower split unless max_context says so.  The partial results of
+ * a split context are joined in a fixed order; they, and so the last bits of o, go by the split. */
 typedef struct gdn_attn_decode_args {
     const void* q;              /* [N,Hq,d] dtype */
     const void* k_cache;
